@@ -383,4 +383,39 @@ int ep_combine_bias(const ep_config_t *cfg, const ep_layout_t *layout, const int
     return ep::launch_combine(a, (hipStream_t)stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
 }
 
+int ep_combine_backward(const ep_config_t *cfg, const ep_layout_t *layout, const int64_t *topk_idx_dev,
+                        const float *topk_weights_dev, const void *y_dev, const void *d_out_dev, void *d_y_dev,
+                        float *d_topk_weights_dev, void *stream) {
+    ep::Shape sh;
+    int rc = make_shape(cfg, &sh);
+    if (rc != EP_OK) return rc;
+    if ((rc = check_layout_ptrs(sh, layout, false)) != EP_OK) return rc;
+    if ((int64_t)sh.S * sh.T > 0) {
+        if (!d_y_dev && !d_topk_weights_dev) return EP_ERR_INVALID_ARG;
+        if (!topk_idx_dev || !aligned(topk_idx_dev, 8) || !d_out_dev || !aligned(d_out_dev, 16) ||
+            (d_y_dev && (!topk_weights_dev || !aligned(topk_weights_dev, 4) || !aligned(d_y_dev, 16))) ||
+            (d_topk_weights_dev && (!y_dev || !aligned(y_dev, 16) || !aligned(d_topk_weights_dev, 4))))
+            return EP_ERR_INVALID_ARG;
+    }
+    ep::CombineBackwardArgs b;
+    b.c.sh = sh;
+    b.c.topk_idx = topk_idx_dev;
+    b.c.topk_weights = d_y_dev ? topk_weights_dev : nullptr;
+    b.c.dst_slot = layout->dst_slot_dev;
+    b.c.recv_psum = layout->recv_psum_dev;
+    b.c.recv_base = layout->recv_base_dev;
+    b.c.expand_pos = layout->expand_pos_dev;
+    b.c.y = d_topk_weights_dev ? static_cast<const uint16_t *>(y_dev) : nullptr;
+    b.c.bias0 = b.c.bias1 = nullptr;
+    b.c.out = nullptr;
+    b.c.y_rows = recv_rows(sh);
+    b.c.slices = 1;
+    b.tokens_per_expert = layout->tokens_per_expert_dev;
+    b.expert_base = layout->expert_base_dev;
+    b.d_out = static_cast<const uint16_t *>(d_out_dev);
+    b.d_y = static_cast<uint16_t *>(d_y_dev);
+    b.d_topk_weights = d_topk_weights_dev;
+    return ep::launch_combine_backward(b, (hipStream_t)stream) == hipSuccess ? EP_OK : EP_ERR_HIP;
+}
+
 }  // extern "C"

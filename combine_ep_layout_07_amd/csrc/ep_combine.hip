@@ -1,7 +1,7 @@
 // ep_combine.hip -- weighted top-k reduction of expert outputs back to token
 // order (the combine reduce epilogue of DeepEP v2, "Add unordered hybrid
 // kernels for transports without ordered delivery" (PR #732), section
-// Changes).
+// Changes), and its gradients (k_combine_backward).
 //
 // out[s][t] = bf16(sum over valid lanes k of w[s][t][k] * Y [+ bias rows]),
 // accumulated in fp32 and rounded to nearest-even once.  In the compact layout
@@ -19,6 +19,7 @@
 // uneven number of rows per token across the resident waves.
 #include "ep_device.h"
 #include "ep_kernels.h"
+#include "ep_wave.h"
 
 namespace ep {
 namespace {
@@ -96,14 +97,16 @@ __device__ __forceinline__ void fma_row(float (&acc)[CPL][8], const u32x4 (&v)[C
 // The distinct rows of token g, one per "row lane": every valid lane in the
 // expand layout; the owner (lowest valid lane) of each rank otherwise, whose
 // weight becomes the lane-ordered fp32 sum over the lanes of its rank.
-// Returns the mask of row lanes; row / wrow hold each row lane's row and weight.
+// Returns the mask of row lanes; row / wrow hold each row lane's row and weight,
+// owner the lane that holds this valid lane's row (-1 on a masked lane).
 // With EARLY_BASES, lane l < R fetches the base of source s in destination l's
 // receive rows together with the ids, so that no load waits for a decoded
 // rank: one dependent load fewer, which matters for short rows only (for
 // 14 KiB rows the four extra registers cost a wave per SIMD: measured 2-3%
 // slower at 4096 tokens, H = 7168).
-template <bool EARLY_BASES>
-__device__ __forceinline__ uint64_t token_rows(const CombineArgs &a, int64_t g, int lane, int &row, float &wrow) {
+template <bool EARLY_BASES, bool BACKWARD = false>
+__device__ __forceinline__ uint64_t token_rows(const CombineArgs &a, int64_t g, int lane, int &row, float &wrow,
+                                               int &owner) {
     const Shape &sh = a.sh;
     const int s = (int)(g / sh.T);
     bool valid = false;
@@ -113,7 +116,7 @@ __device__ __forceinline__ uint64_t token_rows(const CombineArgs &a, int64_t g, 
         const int64_t e64 = a.topk_idx[g * sh.K + lane];
         valid = e64 >= 0 && e64 < sh.E;
         e = valid ? (int)e64 : 0;
-        w = a.topk_weights[g * sh.K + lane];
+        if (!BACKWARD || a.topk_weights) w = a.topk_weights[g * sh.K + lane];
         if (sh.expand) pos = a.expand_pos[g * sh.K + lane];
         else slot = a.dst_slot[g * sh.K + lane];
     }
@@ -126,11 +129,13 @@ __device__ __forceinline__ uint64_t token_rows(const CombineArgs &a, int64_t g, 
     if (sh.expand) {
         row = valid ? pos : -1;
         wrow = w;
+        owner = valid ? lane : -1;
     } else {
         const int d = valid ? rank_of(sh, e) : 0;
         const uint64_t peers = match_key((uint32_t)d, sh.bits_R, vmask);
-        const int owner = peers ? __builtin_ctzll(peers) : 0;
-        const bool is_owner = valid && owner == lane;
+        const int first = peers ? __builtin_ctzll(peers) : 0;
+        const bool is_owner = valid && first == lane;
+        owner = valid ? first : -1;
         if (EARLY_BASES) {
             const int base_d = shfl(base_l, d);
             if (is_owner) row = base_d + (slot - row_base(sh, s) * sh.Nmax);
@@ -140,7 +145,7 @@ __device__ __forceinline__ uint64_t token_rows(const CombineArgs &a, int64_t g, 
         for (uint64_t m = vmask; m; m &= m - 1) {
             const int k = __builtin_ctzll(m);
             const float wk = __int_as_float(read_lane(__float_as_int(w), k));
-            const int ok = read_lane(owner, k);
+            const int ok = read_lane(first, k);
             if (lane == ok) wrow += wk;
         }
     }
@@ -169,9 +174,9 @@ __global__ void __launch_bounds__(kThreads) k_combine(CombineArgs a) {
         const int c_lo = (int)(unit - g * slices) * cps;
         const int c_hi = min(c_lo + cps, nchunks);
         if (c_lo >= c_hi) continue;
-        int row;
+        int row, owner;
         float wrow;
-        const uint64_t rows_mask = token_rows<CPL == 1>(a, g, lane, row, wrow);
+        const uint64_t rows_mask = token_rows<CPL == 1>(a, g, lane, row, wrow, owner);
         const int wbits = __float_as_int(wrow);
         uint16_t *out = a.out + g * sh.H;
         for (int c0 = c_lo; c0 < c_hi; c0 += CPL * kWave) {
@@ -254,7 +259,133 @@ hipError_t run(const CombineArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Gradients of the combine.  Every filled row belongs to one token, so a
+// token's WPT waves read its d_out row once and, chunk by chunk, each of its
+// rows of y (for the weights' dot products, fp32, reduced over the wave and
+// then over the waves in order) and write the row of d_y: a pure stream of
+// 2 * H * (1 + 2 * rows) bytes per token.
+template <int WPT>
+__global__ void __launch_bounds__(kThreads) k_combine_backward(CombineBackwardArgs b) {
+    constexpr int G = kRowsPerGroup;
+    constexpr int kTokens = kWavesPerBlock / WPT;
+    const CombineArgs &a = b.c;
+    const Shape &sh = a.sh;
+    __shared__ float parts[kWavesPerBlock][kWave];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int part = wave % WPT;
+    const int64_t n_tok = (int64_t)sh.S * sh.T;
+    const int nchunks = sh.H / 8;
+    for (int64_t g0 = (int64_t)blockIdx.x * kTokens; g0 < n_tok; g0 += (int64_t)gridDim.x * kTokens) {
+        const int64_t g = g0 + wave / WPT;
+        float dot = 0.0f;
+        int owner = -1;
+        if (g < n_tok) {
+            int row;
+            float wrow;
+            const uint64_t rows_mask = token_rows<false, true>(a, g, lane, row, wrow, owner);
+            const int wbits = __float_as_int(wrow);
+            const uint16_t *dout = b.d_out + g * sh.H;
+            for (uint64_t m = rows_mask; m;) {
+                int rr[G], kk[G], n = 0;
+                float ww[G], acc[G];
+#pragma unroll
+                for (int j = 0; j < G; ++j) {
+                    rr[j] = 0, kk[j] = 0, ww[j] = 0.0f, acc[j] = 0.0f;
+                    if (m) {
+                        kk[j] = __builtin_ctzll(m);
+                        m &= m - 1;
+                        rr[j] = read_lane(row, kk[j]);
+                        ww[j] = __int_as_float(read_lane(wbits, kk[j]));
+                        n = j + 1;
+                    }
+                }
+                for (int c = part * kWave + lane; c < nchunks; c += WPT * kWave) {
+                    const u32x4 d = *reinterpret_cast<const u32x4 *>(dout + (int64_t)c * 8);
+                    u32x4 v[G];
+                    if (a.y) {
+#pragma unroll
+                        for (int j = 0; j < G; ++j)
+                            if (j < n) v[j] = ld16(a.y + (int64_t)rr[j] * sh.H + (int64_t)c * 8);
+                    }
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        if (j >= n) continue;
+                        if (a.y) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                acc[j] = fmaf(bf16_lo(v[j][q]), bf16_lo(d[q]), acc[j]);
+                                acc[j] = fmaf(bf16_hi(v[j][q]), bf16_hi(d[q]), acc[j]);
+                            }
+                        }
+                        if (b.d_y) {
+                            u32x4 o;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) o[q] = pack_bf16(ww[j] * bf16_lo(d[q]), ww[j] * bf16_hi(d[q]));
+                            __builtin_nontemporal_store(
+                                o, reinterpret_cast<u32x4 *>(b.d_y + (int64_t)rr[j] * sh.H + (int64_t)c * 8));
+                        }
+                    }
+                }
+                if (a.y) {
+#pragma unroll
+                    for (int j = 0; j < G; ++j) {
+                        if (j >= n) continue;
+                        const float t = wave_sum(acc[j]);
+                        if (lane == kk[j]) dot = t;
+                    }
+                }
+            }
+        }
+        if (!b.d_topk_weights) continue;
+        if (WPT > 1) {
+            __syncthreads();  // the previous token's parts are read
+            parts[wave][lane] = dot;
+            __syncthreads();
+            dot = 0.0f;
+            for (int w = 0; w < WPT; ++w) dot += parts[wave - part + w][lane];
+        }
+        const float mine = __int_as_float(shfl(__float_as_int(dot), owner >= 0 ? owner : lane));
+        if (g < n_tok && part == 0 && lane < sh.K) b.d_topk_weights[g * sh.K + lane] = owner >= 0 ? mine : 0.0f;
+    }
+}
+
+// Padding rows of d_y (expand layout, alignment > 1): zeros, so that sums over
+// an expert's segment see no gradient there.
+__global__ void __launch_bounds__(kThreads) k_combine_backward_padding(CombineBackwardArgs b) {
+    const Shape &sh = b.c.sh;
+    const int e = blockIdx.x;
+    int cnt = 0;
+    for (int s = 0; s < sh.S; ++s) cnt += b.tokens_per_expert[(int64_t)s * sh.E + e];
+    const int64_t r0 = (int64_t)b.expert_base[e] + cnt;
+    const int64_t r1 = min((int64_t)b.expert_base[e + 1], b.c.y_rows);
+    for (int64_t r = r0 + blockIdx.y; r < r1; r += gridDim.y)
+        for (int c = threadIdx.x; c < sh.H / 8; c += kThreads)
+            *reinterpret_cast<u32x4 *>(b.d_y + r * sh.H + (int64_t)c * 8) = u32x4{0u, 0u, 0u, 0u};
+}
+
 }  // namespace
+
+hipError_t launch_combine_backward(const CombineBackwardArgs &b, hipStream_t stream) {
+    const Shape &sh = b.c.sh;
+    const int64_t n_tok = (int64_t)sh.S * sh.T;
+    if (n_tok > 0) {
+        // A row of one pass of one wave stays with that wave; a longer one is
+        // split over the workgroup's four.
+        const bool wide = sh.H / 8 > kWave;
+        const int64_t want = wide ? n_tok : (n_tok + kWavesPerBlock - 1) / kWavesPerBlock;
+        const int blocks = (int)(want < EP_COMBINE_MAX_BLOCKS ? want : EP_COMBINE_MAX_BLOCKS);
+        if (wide) hipLaunchKernelGGL(k_combine_backward<kWavesPerBlock>, dim3(blocks), dim3(kThreads), 0, stream, b);
+        else hipLaunchKernelGGL(k_combine_backward<1>, dim3(blocks), dim3(kThreads), 0, stream, b);
+        const hipError_t rc = hipGetLastError();
+        if (rc != hipSuccess) return rc;
+    }
+    if (sh.expand && sh.A > 1 && b.d_y) {
+        const int split = sh.A - 1 < 16 ? sh.A - 1 : 16;
+        hipLaunchKernelGGL(k_combine_backward_padding, dim3(sh.E, split), dim3(kThreads), 0, stream, b);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
 
 hipError_t launch_combine(const CombineArgs &args, hipStream_t stream) {
     if ((int64_t)args.sh.S * args.sh.T == 0) return hipSuccess;

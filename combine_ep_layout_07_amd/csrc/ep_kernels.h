@@ -138,6 +138,38 @@ struct CombineArgs {
     int slices;      // column slices per token (set by the launcher)
 };
 
+struct CombineBackwardArgs {
+    CombineArgs c;  // y null: no d_topk_weights; topk_weights null: no d_y
+    const int32_t *tokens_per_expert, *expert_base;  // padding rows (expand layout)
+    const uint16_t *d_out;
+    uint16_t *d_y;           // null: not wanted
+    float *d_topk_weights;   // null: not wanted
+};
+
+// Blocks of the router's forward pass over all sources, at most (each leaves
+// partial sums for the balance loss).
+constexpr int kRouteMaxBlocks = 1024;
+int route_blocks(int S, int T);
+
+struct RouteArgs {
+    int S, T, E, K;
+    int logits_bf16, sigmoid;
+    int vec;  // rows can be loaded in whole lanes (set by the launcher)
+    float scale;
+    const void *logits;
+    const float *bias;          // or null
+    const uint8_t *token_mask;  // or null
+    int64_t *topk_idx;
+    float *topk_weights;
+    int32_t *tokens_per_expert, *tokens_valid;
+    float *balance_loss;
+    float *part_p;       // scratch [S*B][E]: sums of p; null without a balance loss
+    int32_t *part_cnt;   // scratch [S*B][E]: chosen lanes
+    int32_t *part_seen;  // scratch [S*B]: valid tokens
+    const float *d_weights, *d_loss;  // backward; either may be null
+    void *d_logits;
+};
+
 hipError_t launch_layout(const LayoutArgs &a, hipStream_t stream);
 // Whether launch_layout takes the one-launch form for these arguments on the
 // current device.
@@ -154,5 +186,8 @@ bool layout_dispatch_is_one_launch(const LayoutArgs &a, const DispatchArgs &da);
 hipError_t launch_layout_dispatch(const LayoutArgs &a, const DispatchArgs &da, hipStream_t stream);
 hipError_t launch_epilogue(const DispatchArgs &a, hipStream_t stream);
 hipError_t launch_combine(const CombineArgs &a, hipStream_t stream);
+hipError_t launch_combine_backward(const CombineBackwardArgs &a, hipStream_t stream);
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs &a, hipStream_t stream);
 
 }  // namespace ep

@@ -1,5 +1,6 @@
 """Python binding of libep (include/ep.h): deterministic MoE expert-parallel
-dispatch layout, dispatch and combine on one MI355X.
+dispatch layout, dispatch and combine on one MI355X, the router before them,
+the experts' products between them and the gradients of all three.
 
 Argument marshalling only: every step runs in the HIP kernels of ``libep.so``.
 PyTorch provides device memory and the current stream.  The functions keep
@@ -24,7 +25,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("EP_LIBRARY") or os.path.join(_HERE, "libep.so")
 
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CAPACITY, EP_ERR_UNSUPPORTED, EP_ERR_HIP = 0, -1, -2, -3, -4
-EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3FN = 0, 1
+EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3FN, EP_DTYPE_FP32 = 0, 1, 2
+EP_SCORING = {"softmax": 0, "sigmoid": 1}
 EP_PHASE_SCATTER, EP_PHASE_EPILOGUE, EP_PHASE_ALL = 1, 2, 3
 EP_FLAG_DIRECT_RECV_X, EP_FLAG_LAYOUT_ONE_LAUNCH = 1, 2
 
@@ -62,6 +64,23 @@ class EpRecvT(ctypes.Structure):
         "recv_src_idx_dev", "recv_topk_idx_dev", "recv_topk_weights_dev")] + [("recv_capacity_rows", ctypes.c_int64)]
 
 
+class EpRouteConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_src_ranks", "num_tokens", "num_experts", "num_topk", "logits_dtype", "scoring")] + [
+            ("scale", ctypes.c_float)]
+
+
+class EpRouteSizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint64) for n in (
+        "topk_idx", "topk_weights", "tokens_per_expert", "tokens_valid", "balance_loss", "scratch")]
+
+
+class EpRouteT(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "topk_idx_dev", "topk_weights_dev", "tokens_per_expert_dev", "tokens_valid_dev", "balance_loss_dev",
+        "scratch_dev")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
@@ -76,8 +95,13 @@ def _load():
                                        ctypes.POINTER(EpRecvT), P]
     lib.ep_combine.argtypes = [ctypes.POINTER(EpConfig), ctypes.POINTER(EpLayoutT), P, P, P, P, P]
     lib.ep_combine_bias.argtypes = [ctypes.POINTER(EpConfig), ctypes.POINTER(EpLayoutT), P, P, P, P, P, P, P]
+    lib.ep_combine_backward.argtypes = [ctypes.POINTER(EpConfig), ctypes.POINTER(EpLayoutT), P, P, P, P, P, P, P]
+    lib.ep_query_route_sizes.argtypes = [ctypes.POINTER(EpRouteConfig), ctypes.POINTER(EpRouteSizes)]
+    lib.ep_route.argtypes = [ctypes.POINTER(EpRouteConfig), P, P, P, ctypes.POINTER(EpRouteT), P]
+    lib.ep_route_backward.argtypes = [ctypes.POINTER(EpRouteConfig), P, P, ctypes.POINTER(EpRouteT), P, P, P, P]
     for f in ("ep_query_sizes", "ep_layout", "ep_layout_no_alloc", "ep_dispatch", "ep_layout_dispatch", "ep_combine",
-              "ep_combine_bias", "ep_version"):
+              "ep_combine_bias", "ep_combine_backward", "ep_query_route_sizes", "ep_route", "ep_route_backward",
+              "ep_version"):
         getattr(lib, f).restype = ctypes.c_int
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_string.restype = ctypes.c_char_p
@@ -334,3 +358,105 @@ def ep_combine_bias(cfg: EpConfig, layout: LayoutBuffers, topk_idx: torch.Tensor
                               _ptr(out, "out", S * T * H * 2), _stream(stream))
     if rc != EP_OK:
         raise EpError(rc, "ep_combine_bias")
+
+
+def ep_combine_backward(cfg: EpConfig, layout: LayoutBuffers, topk_idx: torch.Tensor,
+                        topk_weights: Optional[torch.Tensor], y: Optional[torch.Tensor], d_out: torch.Tensor,
+                        d_y: Optional[torch.Tensor], d_weights: Optional[torch.Tensor], stream=None) -> None:
+    """Gradients of ep_combine: bf16 d_y in the receive row order and fp32 d_weights [S][T][K]; either may be None."""
+    S, T, K, H = cfg.num_src_ranks, cfg.num_tokens, cfg.num_topk, cfg.hidden
+    rows = _recv_rows(cfg)
+    if topk_idx.dtype != torch.int64 or any(t is not None and t.dtype != torch.float32 for t in (topk_weights, d_weights)):
+        raise ValueError("topk_idx must be int64, topk_weights and d_weights float32")
+    for t, name in ((y, "y"), (d_out, "d_out"), (d_y, "d_y")):
+        _check_elem(t, name, 2)
+    rc = _lib.ep_combine_backward(
+        ctypes.byref(cfg), ctypes.byref(layout.struct), _ptr(topk_idx, "topk_idx", S * T * K * 8),
+        _ptr(topk_weights, "topk_weights", S * T * K * 4 if d_y is not None else 0),
+        _ptr(y, "y", rows * H * 2 if d_weights is not None else 0), _ptr(d_out, "d_out", S * T * H * 2),
+        _ptr(d_y, "d_y", rows * H * 2 if d_y is not None else 0),
+        _ptr(d_weights, "d_weights", S * T * K * 4 if d_weights is not None else 0), _stream(stream))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_combine_backward")
+
+
+def make_route_config(S: int, T: int, E: int, K: int, dtype: str = "fp32", scoring: str = "softmax",
+                      scale: float = 1.0) -> EpRouteConfig:
+    """Router of S sources of T tokens: logits of ``dtype`` ("fp32", "bf16"), ``scoring`` "softmax" or "sigmoid"."""
+    if dtype not in ("fp32", "bf16") or scoring not in EP_SCORING:
+        raise ValueError(f"dtype {dtype!r} or scoring {scoring!r} is not one of fp32, bf16; softmax, sigmoid")
+    return EpRouteConfig(S, T, E, K, EP_DTYPE_BF16 if dtype == "bf16" else EP_DTYPE_FP32, EP_SCORING[scoring], scale)
+
+
+def ep_query_route_sizes(cfg: EpRouteConfig) -> EpRouteSizes:
+    sz = EpRouteSizes()
+    rc = _lib.ep_query_route_sizes(ctypes.byref(cfg), ctypes.byref(sz))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_query_route_sizes")
+    return sz
+
+
+class RouteBuffers:
+    """Device tensors the router writes plus the ep_route_t that points at them; with ``balance`` the counts per
+    expert, the valid tokens and the balance loss of each source too."""
+
+    def __init__(self, cfg: EpRouteConfig, balance: bool = False, device="cuda"):
+        sz = ep_query_route_sizes(cfg)
+        S, T, E, K = cfg.num_src_ranks, cfg.num_tokens, cfg.num_experts, cfg.num_topk
+        self.topk_idx = torch.empty((S, T, K), dtype=torch.int64, device=device)
+        self.topk_weights = torch.empty((S, T, K), dtype=torch.float32, device=device)
+        self.tokens_per_expert = torch.empty((S, E), dtype=torch.int32, device=device) if balance else None
+        self.tokens_valid = torch.empty((S,), dtype=torch.int32, device=device) if balance else None
+        self.balance_loss = torch.empty((S,), dtype=torch.float32, device=device) if balance else None
+        self.scratch = _empty(sz.scratch, torch.int32, device) if balance else None
+        self.struct = EpRouteT(
+            _ptr(self.topk_idx, "topk_idx"), _ptr(self.topk_weights, "topk_weights"),
+            _ptr(self.tokens_per_expert, "tokens_per_expert"), _ptr(self.tokens_valid, "tokens_valid"),
+            _ptr(self.balance_loss, "balance_loss"), _ptr(self.scratch, "scratch"))
+
+
+def alloc_route(cfg: EpRouteConfig, balance: bool = False, device="cuda") -> RouteBuffers:
+    return RouteBuffers(cfg, balance, device)
+
+
+def _logits_ptr(cfg: EpRouteConfig, t: torch.Tensor, name: str) -> Optional[int]:
+    want = torch.bfloat16 if cfg.logits_dtype == EP_DTYPE_BF16 else torch.float32
+    if t.dtype != want:
+        raise ValueError(f"{name} must be {want}, got {t.dtype}")
+    return _ptr(t, name, cfg.num_src_ranks * cfg.num_tokens * cfg.num_experts * t.element_size())
+
+
+def _mask_ptr(cfg: EpRouteConfig, t: Optional[torch.Tensor]) -> Optional[int]:
+    if t is None:
+        return None
+    if t.element_size() != 1:
+        raise ValueError(f"token_mask must have 1-byte elements, got {t.dtype}")
+    return _ptr(t, "token_mask", cfg.num_src_ranks * cfg.num_tokens)
+
+
+def ep_route(cfg: EpRouteConfig, logits: torch.Tensor, route: RouteBuffers, bias: Optional[torch.Tensor] = None,
+             token_mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """topk_idx and topk_weights of ``logits`` [S][T][E] (and the balance loss, if ``route`` has it)."""
+    if bias is not None and bias.dtype != torch.float32:
+        raise ValueError("bias must be float32")
+    rc = _lib.ep_route(ctypes.byref(cfg), _logits_ptr(cfg, logits, "logits"),
+                       _ptr(bias, "bias", cfg.num_experts * 4 if bias is not None else 0),
+                       _mask_ptr(cfg, token_mask), ctypes.byref(route.struct), _stream(stream))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_route")
+
+
+def ep_route_backward(cfg: EpRouteConfig, logits: torch.Tensor, route: RouteBuffers,
+                      d_weights: Optional[torch.Tensor], d_loss: Optional[torch.Tensor], d_logits: torch.Tensor,
+                      token_mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradient of the logits from those of the weights [S][T][K] and of the balance losses [S]; either may be None."""
+    S, T, K = cfg.num_src_ranks, cfg.num_tokens, cfg.num_topk
+    if any(t is not None and t.dtype != torch.float32 for t in (d_weights, d_loss)):
+        raise ValueError("d_weights and d_loss must be float32")
+    rc = _lib.ep_route_backward(ctypes.byref(cfg), _logits_ptr(cfg, logits, "logits"), _mask_ptr(cfg, token_mask),
+                                ctypes.byref(route.struct),
+                                _ptr(d_weights, "d_weights", S * T * K * 4 if d_weights is not None else 0),
+                                _ptr(d_loss, "d_loss", S * 4 if d_loss is not None else 0),
+                                _logits_ptr(cfg, d_logits, "d_logits"), _stream(stream))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_route_backward")

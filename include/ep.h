@@ -1,7 +1,8 @@
 /*
  * ep.h -- C ABI of libep: deterministic MoE expert-parallel dispatch layout,
  * dispatch (scatter + copy epilogue) and combine on one GPU's share of the
- * work, as HIP kernels for CDNA4 (gfx950).
+ * work, the router before it, the experts' products inside it and the
+ * gradients of all three, as HIP kernels for CDNA4 (gfx950).
  *
  * Sources (DeepEP v2 pages):
  *   [DET] "DeepEP v2: Kernel-side deterministic dispatch for the non-expand
@@ -55,7 +56,8 @@ enum ep_status {
 
 enum ep_dtype {
     EP_DTYPE_BF16 = 0,        /* rows of H bf16                                */
-    EP_DTYPE_FP8_E4M3FN = 1   /* rows of H OCP e4m3fn bytes + H/128 fp32 scales */
+    EP_DTYPE_FP8_E4M3FN = 1,  /* rows of H OCP e4m3fn bytes + H/128 fp32 scales */
+    EP_DTYPE_FP32 = 2         /* the router's logits only                      */
 };
 
 /* Phases of ep_dispatch.  The pages time the sender's dispatch kernel and the
@@ -314,6 +316,96 @@ int ep_combine(const ep_config_t *cfg, const ep_layout_t *layout, const int64_t 
 int ep_combine_bias(const ep_config_t *cfg, const ep_layout_t *layout, const int64_t *topk_idx_dev,
                     const float *topk_weights_dev, const void *y_dev, const void *bias0_dev,
                     const void *bias1_dev, void *out_dev, void *stream);
+
+/* Gradients of ep_combine for the y_dev of that call and the gradient d_out of
+ * its output (ep_combine_bias has the same ones, and d_out is the gradient of
+ * each bias tensor):
+ *   d_y[row] = bf16(w_row * d_out[s][t]), w_row the fp32 sum in ascending lane
+ *              order of the weights of the lanes of (s,t) that read the row
+ *              (one lane in the expand layout), so every filled row has exactly
+ *              one token and is written once; padding rows of an expand layout
+ *              with alignment > 1 are written as zeros, rows beyond the filled
+ *              ones are left untouched;
+ *   d_topk_weights[s][t][k] = fp32 sum over the row of Y(s,t,k) * d_out[s][t]
+ *              on a valid lane, +0 on a masked one.  The order of the sum is
+ *              fixed: results are bitwise reproducible.
+ * Either gradient may be NULL (not both); y_dev is needed for d_topk_weights
+ * only and topk_weights_dev for d_y only.  bf16 d_y_dev [rows][H], d_out_dev
+ * [S][T][H], y_dev as in ep_combine; 16-byte aligned. */
+int ep_combine_backward(const ep_config_t *cfg, const ep_layout_t *layout, const int64_t *topk_idx_dev,
+                        const float *topk_weights_dev, const void *y_dev, const void *d_out_dev, void *d_y_dev,
+                        float *d_topk_weights_dev, void *stream);
+
+/* ---- Router: the topk_idx and topk_weights that ep_layout, ep_dispatch and
+ * ep_combine take, from the logits of S x T tokens over E experts. ---- */
+
+enum ep_scoring {
+    EP_SCORING_SOFTMAX = 0, /* s = exp(l - max) / sum over the token's experts */
+    EP_SCORING_SIGMOID = 1  /* s = 1 / (1 + exp(-l))                           */
+};
+
+/* Limits as above: 1 <= K <= 32, K <= E <= 1024, S <= 65535, T <= 2^30,
+ * S * T * K < 2^31. */
+typedef struct ep_route_config {
+    int32_t num_src_ranks;  /* S >= 1                                          */
+    int32_t num_tokens;     /* T >= 0, tokens per source                       */
+    int32_t num_experts;    /* E                                               */
+    int32_t num_topk;       /* K <= E                                          */
+    int32_t logits_dtype;   /* EP_DTYPE_FP32 or EP_DTYPE_BF16                  */
+    int32_t scoring;        /* enum ep_scoring                                 */
+    float scale;            /* finite; the weights of a token sum to it        */
+} ep_route_config_t;
+
+/* Byte sizes of the buffers of ep_route_t. */
+typedef struct ep_route_sizes {
+    uint64_t topk_idx, topk_weights, tokens_per_expert, tokens_valid, balance_loss, scratch;
+} ep_route_sizes_t;
+
+/* Outputs of ep_route.  tokens_per_expert, tokens_valid, balance_loss and
+ * scratch serve the balance loss: all four, or all NULL.
+ *   topk_idx          int64 [S][T][K], best first; -1 on the lanes of a token
+ *                     with fewer than K valid experts
+ *   topk_weights      fp32 [S][T][K], scale * s_k / (sum of s_k + 1e-20); +0
+ *                     on a lane of -1
+ *   tokens_per_expert int32 [S][E], lanes of source s that chose expert e
+ *   tokens_valid      int32 [S], tokens with a valid expert, V
+ *   balance_loss      fp32 [S], sum over e of f_e * P_e with
+ *                     f_e = tokens_per_expert[e] * E / (K * max(V, 1)) and
+ *                     P_e = sum over tokens of p_e / max(V, 1); p = s (softmax)
+ *                     or s / (sum of the token's s + 1e-20) (sigmoid)
+ *   scratch           8-byte aligned, private to the library, needs no
+ *                     initialisation */
+typedef struct ep_route {
+    int64_t *topk_idx_dev;
+    float *topk_weights_dev;
+    int32_t *tokens_per_expert_dev;
+    int32_t *tokens_valid_dev;
+    float *balance_loss_dev;
+    void *scratch_dev;
+} ep_route_t;
+
+int ep_query_route_sizes(const ep_route_config_t *cfg, ep_route_sizes_t *sizes);
+
+/* Scores, choice and weights.  An expert of a token is valid if the token's
+ * mask byte is not 0 (token_mask_dev uint8 [S][T], may be NULL) and its logit is
+ * above the type's lowest value: -inf, that value and NaN are masked; +inf
+ * counts as the type's largest value.  The K experts are those with the largest
+ * key, ties to the lowest index.  Without a bias (bias_dev NULL) the key is the
+ * logit; with one (fp32 [E]) it is s + bias[e] to 64-bit accuracy, so that the
+ * choice does not depend on rounding; an expert whose bias is NaN or -inf is
+ * not chosen.  The weights use s without the bias. */
+int ep_route(const ep_route_config_t *cfg, const void *logits_dev, const float *bias_dev,
+             const uint8_t *token_mask_dev, const ep_route_t *route, void *stream);
+
+/* Gradient of the logits (same type, [S][T][E]) from the gradients of the
+ * weights (d_topk_weights_dev fp32 [S][T][K], may be NULL) and of the balance
+ * losses (d_balance_loss_dev fp32 [S], may be NULL; needs the counts), of the
+ * ep_route call with the same logits, mask and route.  The choice and the
+ * counts are constants; masked experts get +0.  Reads topk_idx,
+ * tokens_per_expert and tokens_valid of *route. */
+int ep_route_backward(const ep_route_config_t *cfg, const void *logits_dev, const uint8_t *token_mask_dev,
+                      const ep_route_t *route, const float *d_topk_weights_dev, const float *d_balance_loss_dev,
+                      void *d_logits_dev, void *stream);
 
 /* Static description of a status code. */
 const char *ep_status_string(int status);
