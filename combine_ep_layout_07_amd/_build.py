@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libep.so")
-SOURCES = ["ep_layout.hip", "ep_dispatch.hip", "ep_combine.hip", "ep_route.hip", "ep_api.cpp", "ep_route_api.cpp"]
+SOURCES = ["ep_layout.hip", "ep_dispatch.hip", "ep_combine.hip", "ep_route.hip", "ep_expert.hip", "ep_api.cpp",
+           "ep_route_api.cpp", "ep_expert_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,102 @@
+// ep_expert.h -- arguments and device helpers of the experts' products.
+#pragma once
+
+#include "ep_wave.h"
+
+namespace ep {
+
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
+
+// Row splits of an expert's segment in the activation's backward pass (each
+// leaves one partial sum per column for d_bias).
+constexpr int kActSplits = 16;
+
+struct ExpertArgs {
+    int E, I, N, Nw;  // Nw = weight rows per expert: 2N for swiglu, else N
+    int act, fp8;
+    int64_t rows;
+    const int32_t *base;  // [E+1]
+    const void *x, *w;
+    const float *x_sf, *w_sf;  // fp8: [rows][I/128], [E][ceil(Nw/128)][I/128]
+    const float *bias;         // [E][Nw] or null
+    const uint16_t *residual;  // [rows][N] or null
+    uint16_t *out;             // [rows][N]
+    uint16_t *pre;             // [rows][Nw] or null; backward: read
+    const uint16_t *d_out;     // backward [rows][N]
+    uint16_t *d;               // scratch [rows][Nw]: gradient of the pre-activation (d_out itself without one)
+    float *part;               // scratch [E][kActSplits][Nw]
+    uint16_t *d_x, *d_w;       // either may be null
+    float *d_bias;             // or null
+};
+
+struct Segment {
+    int e;       // -1: none
+    int64_t r0;  // first row
+    int n;       // rows
+};
+
+// Rows of expert e, inside [0, rows] whatever the table holds.
+__device__ __forceinline__ Segment segment_of(const int32_t *base, int e, int64_t rows) {
+    const int64_t lo = base[e], hi = base[e + 1];
+    const int64_t a = lo < 0 ? 0 : (lo < rows ? lo : rows);
+    const int64_t b = hi < a ? a : (hi < rows ? hi : rows);
+    return {e, a, (int)(b - a)};
+}
+
+// Tile `tile` of `size` rows, counted over the experts in order: a scan over
+// the experts by the whole wave, 64 at a time.
+__device__ __forceinline__ Segment find_tile(const int32_t *base, int E, int64_t rows, int size, int64_t tile) {
+    const int lane = lane_id();
+    int64_t before = 0;
+    for (int e0 = 0; e0 < E; e0 += kWave) {
+        const int e = e0 + lane;
+        const Segment g = e < E ? segment_of(base, e, rows) : Segment{e, 0, 0};
+        const int mine = (g.n + size - 1) / size;
+        int incl = mine;
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int v = shfl(incl, lane - d < 0 ? lane : lane - d);
+            if (lane >= d) incl += v;
+        }
+        const uint64_t past = ballot(before + incl > tile);
+        if (past) {
+            const int o = __builtin_ctzll(past);
+            const int64_t at = tile - before - (read_lane(incl, o) - read_lane(mine, o));
+            const int64_t r0 = (int64_t)read_lane((int)g.r0, o) + at * size;
+            const int64_t left = read_lane(g.n, o) - at * size;
+            return {e0 + o, r0, (int)(left < size ? left : size)};
+        }
+        before += read_lane(incl, kWave - 1);
+    }
+    return {-1, 0, 0};
+}
+
+// 1 / (1 + exp(-v)) without overflow on either side.
+__device__ __forceinline__ float logistic(float v) {
+    const float z = expf(-fabsf(v));
+    return (v >= 0.0f ? 1.0f : z) / (1.0f + z);
+}
+
+// The activations of one argument.
+__device__ __forceinline__ float activate(int act, float v) {
+    if (act == kActRelu) return v < 0.0f ? 0.0f : v;
+    if (act == kActGelu) return 0.5f * v * erfcf(v * -0.70710678118654752f);
+    if (act == kActSilu) return v * logistic(v);
+    return v;
+}
+// Their derivatives.
+__device__ __forceinline__ float activate_slope(int act, float v) {
+    if (act == kActRelu) return v > 0.0f ? 1.0f : 0.0f;
+    if (act == kActGelu)
+        return 0.5f * erfcf(v * -0.70710678118654752f) + v * expf(-0.5f * v * v) * 0.39894228040143268f;
+    if (act == kActSilu) {
+        const float s = logistic(v);
+        return s * (1.0f + v * (1.0f - s));
+    }
+    return 1.0f;
+}
+
+hipError_t launch_expert(const ExpertArgs &a, hipStream_t st);
+hipError_t launch_expert_backward(const ExpertArgs &a, hipStream_t st);
+
+}  // namespace ep

@@ -27,6 +27,7 @@ LIB_PATH = os.environ.get("EP_LIBRARY") or os.path.join(_HERE, "libep.so")
 EP_OK, EP_ERR_INVALID_ARG, EP_ERR_CAPACITY, EP_ERR_UNSUPPORTED, EP_ERR_HIP = 0, -1, -2, -3, -4
 EP_DTYPE_BF16, EP_DTYPE_FP8_E4M3FN, EP_DTYPE_FP32 = 0, 1, 2
 EP_SCORING = {"softmax": 0, "sigmoid": 1}
+EP_ACTIVATION = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 EP_PHASE_SCATTER, EP_PHASE_EPILOGUE, EP_PHASE_ALL = 1, 2, 3
 EP_FLAG_DIRECT_RECV_X, EP_FLAG_LAYOUT_ONE_LAUNCH = 1, 2
 
@@ -81,6 +82,17 @@ class EpRouteT(ctypes.Structure):
         "scratch_dev")]
 
 
+class EpExpertConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_experts", "in_features", "out_features", "x_dtype", "activation", "reserved")] + [
+            ("num_rows", ctypes.c_int64)]
+
+
+class EpExpertSizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint64) for n in (
+        "x", "x_sf", "w", "w_sf", "bias", "out", "pre", "backward_scratch")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
@@ -99,9 +111,12 @@ def _load():
     lib.ep_query_route_sizes.argtypes = [ctypes.POINTER(EpRouteConfig), ctypes.POINTER(EpRouteSizes)]
     lib.ep_route.argtypes = [ctypes.POINTER(EpRouteConfig), P, P, P, ctypes.POINTER(EpRouteT), P]
     lib.ep_route_backward.argtypes = [ctypes.POINTER(EpRouteConfig), P, P, ctypes.POINTER(EpRouteT), P, P, P, P]
+    lib.ep_query_expert_sizes.argtypes = [ctypes.POINTER(EpExpertConfig), ctypes.POINTER(EpExpertSizes)]
+    lib.ep_expert_mm.argtypes = [ctypes.POINTER(EpExpertConfig)] + [P] * 10
+    lib.ep_expert_mm_backward.argtypes = [ctypes.POINTER(EpExpertConfig)] + [P] * 10
     for f in ("ep_query_sizes", "ep_layout", "ep_layout_no_alloc", "ep_dispatch", "ep_layout_dispatch", "ep_combine",
               "ep_combine_bias", "ep_combine_backward", "ep_query_route_sizes", "ep_route", "ep_route_backward",
-              "ep_version"):
+              "ep_query_expert_sizes", "ep_expert_mm", "ep_expert_mm_backward", "ep_version"):
         getattr(lib, f).restype = ctypes.c_int
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_string.restype = ctypes.c_char_p
@@ -460,3 +475,85 @@ def ep_route_backward(cfg: EpRouteConfig, logits: torch.Tensor, route: RouteBuff
                                 _logits_ptr(cfg, d_logits, "d_logits"), _stream(stream))
     if rc != EP_OK:
         raise EpError(rc, "ep_route_backward")
+
+
+def make_expert_config(E: int, rows: int, I: int, N: int, dtype: str = "bf16", activation: str = "none") -> EpExpertConfig:
+    """Products of ``rows`` rows of I features, grouped by E experts, to N features; ``dtype`` "bf16" or "fp8"."""
+    if dtype not in ("bf16", "fp8") or activation not in EP_ACTIVATION:
+        raise ValueError(f"dtype {dtype!r} or activation {activation!r} is not one of bf16, fp8; {', '.join(EP_ACTIVATION)}")
+    return EpExpertConfig(E, I, N, EP_DTYPE_FP8_E4M3FN if dtype == "fp8" else EP_DTYPE_BF16, EP_ACTIVATION[activation],
+                          0, rows)
+
+
+def ep_query_expert_sizes(cfg: EpExpertConfig) -> EpExpertSizes:
+    sz = EpExpertSizes()
+    rc = _lib.ep_query_expert_sizes(ctypes.byref(cfg), ctypes.byref(sz))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_query_expert_sizes")
+    return sz
+
+
+def _expert_sizes(cfg: EpExpertConfig) -> EpExpertSizes:
+    """ep_query_expert_sizes, kept on cfg with the bytes it was computed from."""
+    key = bytes(cfg)
+    memo = getattr(cfg, "_sizes_memo", None)
+    if memo is None or memo[0] != key:
+        memo = (key, ep_query_expert_sizes(cfg))
+        cfg._sizes_memo = memo
+    return memo[1]
+
+
+def alloc_expert_backward(cfg: EpExpertConfig, device="cuda") -> torch.Tensor:
+    """Scratch of ep_expert_mm_backward; one that is not in use may serve any call of the same configuration."""
+    return torch.empty(max(1, int(_expert_sizes(cfg).backward_scratch)), dtype=torch.uint8, device=device)
+
+
+def _base_ptr(cfg: EpExpertConfig, t: torch.Tensor) -> Optional[int]:
+    if t.dtype != torch.int32:
+        raise ValueError("expert_base must be int32")
+    return _ptr(t, "expert_base", (cfg.num_experts + 1) * 4)
+
+
+def _opt(t: Optional[torch.Tensor], name: str, nbytes: int, size: int) -> Optional[int]:
+    """Pointer of an optional tensor of ``size``-byte elements (4: float32)."""
+    if t is None:
+        return None
+    if size == 4 and t.dtype != torch.float32:
+        raise ValueError(f"{name} must be float32")
+    _check_elem(t, name, size)
+    return _ptr(t, name, nbytes)
+
+
+def ep_expert_mm(cfg: EpExpertConfig, expert_base: torch.Tensor, x: torch.Tensor, w: torch.Tensor, out: torch.Tensor,
+                 x_sf: Optional[torch.Tensor] = None, w_sf: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                 pre: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out = act(x W_e^T + bias) + residual over rows grouped by expert; ``pre`` keeps the pre-activation."""
+    sz = _expert_sizes(cfg)
+    el = 1 if cfg.x_dtype == EP_DTYPE_FP8_E4M3FN else 2
+    _check_elem(x, "x", el)
+    _check_elem(w, "w", el)
+    _check_elem(out, "out", 2)
+    rc = _lib.ep_expert_mm(
+        ctypes.byref(cfg), _base_ptr(cfg, expert_base), _ptr(x, "x", sz.x), _opt(x_sf, "x_sf", sz.x_sf, 4),
+        _ptr(w, "w", sz.w), _opt(w_sf, "w_sf", sz.w_sf, 4), _opt(bias, "bias", sz.bias, 4),
+        _opt(residual, "residual", sz.out, 2), _ptr(out, "out", sz.out), _opt(pre, "pre", sz.pre, 2), _stream(stream))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_expert_mm")
+
+
+def ep_expert_mm_backward(cfg: EpExpertConfig, expert_base: torch.Tensor, x: Optional[torch.Tensor], w: torch.Tensor,
+                          d_out: torch.Tensor, scratch: torch.Tensor, pre: Optional[torch.Tensor] = None,
+                          d_x: Optional[torch.Tensor] = None, d_w: Optional[torch.Tensor] = None,
+                          d_bias: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of a bf16 ep_expert_mm, each optional, from that of its output and the kept pre-activation."""
+    sz = _expert_sizes(cfg)
+    _check_elem(w, "w", 2)
+    _check_elem(d_out, "d_out", 2)
+    rc = _lib.ep_expert_mm_backward(
+        ctypes.byref(cfg), _base_ptr(cfg, expert_base), _opt(x, "x", sz.x, 2), _ptr(w, "w", sz.w),
+        _opt(pre, "pre", sz.pre, 2), _ptr(d_out, "d_out", sz.out), _opt(d_x, "d_x", sz.x, 2),
+        _opt(d_w, "d_w", sz.w, 2), _opt(d_bias, "d_bias", sz.bias, 4),
+        _ptr(scratch, "scratch", sz.backward_scratch), _stream(stream))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_expert_mm_backward")

@@ -407,6 +407,75 @@ int ep_route_backward(const ep_route_config_t *cfg, const void *logits_dev, cons
                       const ep_route_t *route, const float *d_topk_weights_dev, const float *d_balance_loss_dev,
                       void *d_logits_dev, void *stream);
 
+/* ---- Experts' products: rows grouped by expert times their expert's weights,
+ * for the receive rows of the expand layout (expert_base) or any other rows
+ * grouped the same way. ---- */
+
+enum ep_activation {
+    EP_ACTIVATION_NONE = 0,
+    EP_ACTIVATION_RELU = 1,
+    EP_ACTIVATION_GELU = 2,   /* v * Phi(v), the exact form                    */
+    EP_ACTIVATION_SILU = 3,   /* v / (1 + exp(-v))                             */
+    EP_ACTIVATION_SWIGLU = 4  /* silu(gate) * up: Nw = 2N weight rows, the gate's
+                                 first                                         */
+};
+
+#define EP_MAX_EXPERT_ROWS 2147483647ll
+
+/* Limits: E <= 1024, I and N <= 262144, N a multiple of 8, I of 8 (bf16) or of
+ * 128 (fp8).  Outside them a call returns EP_ERR_UNSUPPORTED. */
+typedef struct ep_expert_config {
+    int32_t num_experts;   /* E                                                */
+    int32_t in_features;   /* I                                                */
+    int32_t out_features;  /* N                                                */
+    int32_t x_dtype;       /* EP_DTYPE_BF16 or EP_DTYPE_FP8_E4M3FN: x and w    */
+    int32_t activation;    /* enum ep_activation                               */
+    int32_t reserved;      /* 0                                                */
+    int64_t num_rows;      /* rows allocated, >= expert_base[E]                */
+} ep_expert_config_t;
+
+/* Byte sizes of the buffers of a configuration (0 = not used). */
+typedef struct ep_expert_sizes {
+    uint64_t x, x_sf, w, w_sf, bias, out, pre, backward_scratch;
+} ep_expert_sizes_t;
+
+int ep_query_expert_sizes(const ep_expert_config_t *cfg, ep_expert_sizes_t *sizes);
+
+/* For each expert e and each of its rows r in [expert_base[e],
+ * expert_base[e+1]):  pre[r] = x[r] W_e^T + bias[e],
+ * out[r] = act(pre[r]) + residual[r].
+ *   expert_base_dev int32 [E+1], not decreasing (an entry outside the rows is
+ *                   taken as the nearest row); other rows are left untouched
+ *   x_dev           [num_rows][I];  w_dev [E][Nw][I], Nw = N, or 2N for swiglu
+ *   x_sf_dev        fp32 [num_rows][I/128] and
+ *   w_sf_dev        fp32 [E][ceil(Nw/128)][I/128], one scale per 128 x 128
+ *                   block: fp8 only, else NULL
+ *   bias_dev        fp32 [E][Nw] or NULL;  residual_dev bf16 [num_rows][N] or
+ *                   NULL (may be out_dev itself)
+ *   out_dev         bf16 [num_rows][N];  pre_dev bf16 [num_rows][Nw] or NULL:
+ *                   the pre-activation that the backward pass reads
+ * Products are summed in fp32, the epilogue works on the fp32 sum, and out and
+ * pre are each rounded once.  All pointers but the scales and expert_base
+ * 16-byte aligned. */
+int ep_expert_mm(const ep_expert_config_t *cfg, const int32_t *expert_base_dev, const void *x_dev,
+                 const float *x_sf_dev, const void *w_dev, const float *w_sf_dev, const float *bias_dev,
+                 const void *residual_dev, void *out_dev, void *pre_dev, void *stream);
+
+/* Gradients of a bf16 ep_expert_mm with d_out (bf16 [num_rows][N]) the gradient
+ * of out (the residual's is d_out itself):
+ *   d = act'(pre) d_out,  d_x[r] = d[r] W_e  (bf16 [num_rows][I]),
+ *   d_w[e] = sum over the expert's rows of d[r]^T x[r]  (bf16 [E][Nw][I]),
+ *   d_bias[e] = sum of d[r]  (fp32 [E][Nw]);
+ * an expert without rows gets zeros.  Each gradient may be NULL (not all).
+ * pre_dev is not needed without an activation, x_dev only for d_w.  The
+ * matrix units take d rounded to bf16; d_bias sums the unrounded values, in a
+ * fixed order.  Padding rows count like others: ep_combine_backward writes
+ * zeros there.  scratch_dev: backward_scratch bytes, contents need no
+ * initialisation. */
+int ep_expert_mm_backward(const ep_expert_config_t *cfg, const int32_t *expert_base_dev, const void *x_dev,
+                          const void *w_dev, const void *pre_dev, const void *d_out_dev, void *d_x_dev, void *d_w_dev,
+                          float *d_bias_dev, void *scratch_dev, void *stream);
+
 /* Static description of a status code. */
 const char *ep_status_string(int status);
 
