@@ -7,9 +7,12 @@ namespace ep {
 
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
 
-// Row splits of an expert's segment in the activation's backward pass (each
-// leaves one partial sum per column for d_bias).
-constexpr int kActSplits = 16;
+// Rows of a tile of the activation's backward pass (each leaves one partial sum
+// per column for d_bias).
+constexpr int kActRows = 64;
+
+// Tiles of `size` rows that E segments of `rows` rows in all can make, at most.
+inline int64_t expert_row_tiles(int64_t rows, int E, int size) { return rows / size + (rows < E ? rows : E); }
 
 struct ExpertArgs {
     int E, I, N, Nw;  // Nw = weight rows per expert: 2N for swiglu, else N
@@ -24,7 +27,8 @@ struct ExpertArgs {
     uint16_t *pre;             // [rows][Nw] or null; backward: read
     const uint16_t *d_out;     // backward [rows][N]
     uint16_t *d;               // scratch [rows][Nw]: gradient of the pre-activation (d_out itself without one)
-    float *part;               // scratch [E][kActSplits][Nw]
+    float *part;               // scratch [part_tiles][Nw]
+    int64_t part_tiles;
     uint16_t *d_x, *d_w;       // either may be null
     float *d_bias;             // or null
 };

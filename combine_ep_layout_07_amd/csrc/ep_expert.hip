@@ -315,48 +315,64 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
 }
 
 // Gradient of the pre-activation, bf16, and the columns' sums of its unrounded
-// values for d_bias.  blockIdx: x = 512 columns of N, y = expert, z = split of
-// its rows; the four waves take rows in turn, and their sums are added in
-// order.
+// values for d_bias.  A workgroup takes 512 columns of one tile of kActRows
+// rows of an expert (so that one expert with most of the rows is no slower),
+// each wave a quarter of the rows, four in flight; the waves' sums are added in
+// order, and a second launch adds the tiles' in order.
 template <bool GATED>
-__global__ void __launch_bounds__(kThreads) k_expert_act_backward(ExpertArgs a) {
-    __shared__ float sum[kThreads / kWave - 1][kWave][GATED ? 17 : 9];
-    const int lane = lane_id(), wave = threadIdx.x / kWave, e = blockIdx.y;
-    const Segment g = segment_of(a.base, e, a.rows);
-    const int each = (g.n + gridDim.z - 1) / gridDim.z;
-    const int lo = min(g.n, (int)blockIdx.z * each), hi = min(g.n, lo + each);
-    const int n = (blockIdx.x * kWave + lane) * 8;
+__global__ void __launch_bounds__(kThreads) k_expert_act_backward(ExpertArgs a, int cols) {
+    constexpr int kMore = kThreads / kWave - 1, kEach = kActRows / (kMore + 1), G = 4;
+    __shared__ float sum[kMore][kWave][GATED ? 17 : 9];
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
+    const int64_t tile = blockIdx.x / cols;
+    const Segment g = find_tile(a.base, a.E, a.rows, kActRows, tile);
+    if (g.e < 0) return;
+    const int n = (blockIdx.x % cols * kWave + lane) * 8;
     float sg[8], su[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) sg[j] = su[j] = 0.0f;
     if (n < a.N)
-        for (int i = lo + wave; i < hi; i += kThreads / kWave) {
-            const int64_t r = g.r0 + i;
-            const u32x4 d = *reinterpret_cast<const u32x4 *>(a.d_out + r * a.N + n);
-            u32x4 v = {0u, 0u, 0u, 0u}, u = v, od, ou;
-            if (a.act != kActNone) v = *reinterpret_cast<const u32x4 *>(a.pre + r * a.Nw + n);
-            if (GATED) u = *reinterpret_cast<const u32x4 *>(a.pre + r * a.Nw + a.N + n);
+        for (int i0 = 0; i0 < kEach; i0 += G) {
+            const int64_t first = g.r0 + wave * kEach + i0;
+            const int left = g.n - wave * kEach - i0;
+            u32x4 d[G], v[G], u[G];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float dg[2], du[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float dv = h ? bf16_hi(d[q]) : bf16_lo(d[q]), p = h ? bf16_hi(v[q]) : bf16_lo(v[q]);
-                    if (GATED) {
-                        const float s = logistic(p), w = h ? bf16_hi(u[q]) : bf16_lo(u[q]);
-                        dg[h] = dv * w * s * (1.0f + p * (1.0f - s));
-                        du[h] = dv * p * s;
-                        su[2 * q + h] += du[h];
-                    } else {
-                        dg[h] = a.act == kActRelu ? (p > 0.0f ? dv : 0.0f) : dv * activate_slope(a.act, p);
-                    }
-                    sg[2 * q + h] += dg[h];
+            for (int i = 0; i < G; ++i) {
+                const int64_t r = first + (i < left ? i : 0);
+                d[i] = v[i] = u[i] = u32x4{0u, 0u, 0u, 0u};
+                if (left > 0) {
+                    d[i] = *reinterpret_cast<const u32x4 *>(a.d_out + r * a.N + n);
+                    if (a.act != kActNone) v[i] = *reinterpret_cast<const u32x4 *>(a.pre + r * a.Nw + n);
+                    if (GATED) u[i] = *reinterpret_cast<const u32x4 *>(a.pre + r * a.Nw + a.N + n);
                 }
-                od[q] = pack_bf16(dg[0], dg[1]);
-                if (GATED) ou[q] = pack_bf16(du[0], du[1]);
             }
-            if (a.act != kActNone) *reinterpret_cast<u32x4 *>(a.d + r * a.Nw + n) = od;
-            if (GATED) *reinterpret_cast<u32x4 *>(a.d + r * a.Nw + a.N + n) = ou;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                if (i >= left) continue;
+                const int64_t r = first + i;
+                u32x4 od, ou;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float dg[2], du[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float dv = h ? bf16_hi(d[i][q]) : bf16_lo(d[i][q]), p = h ? bf16_hi(v[i][q]) : bf16_lo(v[i][q]);
+                        if (GATED) {
+                            const float s = logistic(p), w = h ? bf16_hi(u[i][q]) : bf16_lo(u[i][q]);
+                            dg[h] = dv * w * s * (1.0f + p * (1.0f - s));
+                            du[h] = dv * p * s;
+                            su[2 * q + h] += du[h];
+                        } else {
+                            dg[h] = a.act == kActRelu ? (p > 0.0f ? dv : 0.0f) : dv * activate_slope(a.act, p);
+                        }
+                        sg[2 * q + h] += dg[h];
+                    }
+                    od[q] = pack_bf16(dg[0], dg[1]);
+                    if (GATED) ou[q] = pack_bf16(du[0], du[1]);
+                }
+                if (a.act != kActNone) *reinterpret_cast<u32x4 *>(a.d + r * a.Nw + n) = od;
+                if (GATED) *reinterpret_cast<u32x4 *>(a.d + r * a.Nw + a.N + n) = ou;
+            }
         }
     if (!a.d_bias) return;
     if (wave > 0)
@@ -367,10 +383,10 @@ __global__ void __launch_bounds__(kThreads) k_expert_act_backward(ExpertArgs a) 
         }
     __syncthreads();
     if (wave > 0 || n >= a.N) return;
-    float *to = gridDim.z == 1 ? a.d_bias + (int64_t)e * a.Nw : a.part + ((int64_t)e * gridDim.z + blockIdx.z) * a.Nw;
+    float *to = a.part + tile * a.Nw;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        for (int w = 0; w < kThreads / kWave - 1; ++w) {
+        for (int w = 0; w < kMore; ++w) {
             sg[j] += sum[w][lane][j];
             if (GATED) su[j] += sum[w][lane][8 + j];
         }
@@ -379,18 +395,31 @@ __global__ void __launch_bounds__(kThreads) k_expert_act_backward(ExpertArgs a) 
     }
 }
 
-__global__ void __launch_bounds__(kThreads) k_expert_bias_sum(ExpertArgs a, int splits) {
-    const int n = blockIdx.x * kThreads + threadIdx.x, e = blockIdx.y;
-    if (n >= a.Nw) return;
+// d_bias: the sums of the expert's tiles, each wave every fourth, then the
+// waves in order.
+__global__ void __launch_bounds__(kThreads) k_expert_bias_sum(ExpertArgs a) {
+    __shared__ float sum[kThreads / kWave][kWave];
+    const int lane = lane_id(), wave = threadIdx.x / kWave, e = blockIdx.y;
+    const int n = blockIdx.x * kWave + lane;
+    const int first = count_tiles(a.base, e, a.rows, kActRows);
+    const int tiles = (segment_of(a.base, e, a.rows).n + kActRows - 1) / kActRows;
+    // (A table that decreases counts more tiles than there are: stay inside.)
+    const int last = (int)min((int64_t)first + tiles, a.part_tiles);
     float s = 0.0f;
-    for (int z = 0; z < splits; ++z) s += a.part[((int64_t)e * splits + z) * a.Nw + n];
+    if (n < a.Nw) {
+#pragma unroll 4
+        for (int t = first + wave; t < last; t += kThreads / kWave) s += a.part[(int64_t)t * a.Nw + n];
+    }
+    sum[wave][lane] = s;
+    __syncthreads();
+    if (wave > 0 || n >= a.Nw) return;
+    for (int w = 1; w < kThreads / kWave; ++w) s += sum[w][lane];
     a.d_bias[(int64_t)e * a.Nw + n] = s;
 }
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tiles of `size` rows that E segments of `rows` rows can make.
-int64_t row_tiles(const ExpertArgs &a, int size) { return a.rows / size + (a.rows < a.E ? a.rows : a.E); }
+int64_t row_tiles(const ExpertArgs &a, int size) { return expert_row_tiles(a.rows, a.E, size); }
 
 template <int MODE, bool FP8, int BQ, int BP, int WQ, int WP>
 hipError_t run_tile(const ExpertArgs &a, hipStream_t st) {
@@ -422,19 +451,19 @@ hipError_t launch_expert_backward(const ExpertArgs &args, hipStream_t st) {
     ExpertArgs a = args;
     hipError_t rc = hipSuccess;
     if (a.act == kActNone) a.d = const_cast<uint16_t *>(a.d_out);
-    if (a.d_bias || a.act != kActNone) {
-        const int cols = ceil_div(a.N, 512);
-        // About 2048 workgroups, at least 16 rows each on average.
-        int splits = 1;
-        while (splits < kActSplits && splits * a.E * cols < 2048 && a.rows / a.E > splits * 32) splits *= 2;
-        const dim3 grid(cols, a.E, splits);
-        if (a.act == kActSwiglu) hipLaunchKernelGGL(k_expert_act_backward<true>, grid, dim3(kThreads), 0, st, a);
-        else hipLaunchKernelGGL(k_expert_act_backward<false>, grid, dim3(kThreads), 0, st, a);
+    if (a.rows > 0 && (a.d_bias || a.act != kActNone)) {
+        const int cols = ceil_div(a.N, kWave * 8);
+        const int64_t blocks = cols * a.part_tiles;
+        if (blocks > 4294967295ll / kThreads) return hipErrorInvalidValue;
+        if (a.act == kActSwiglu)
+            hipLaunchKernelGGL(k_expert_act_backward<true>, dim3((uint32_t)blocks), dim3(kThreads), 0, st, a, cols);
+        else
+            hipLaunchKernelGGL(k_expert_act_backward<false>, dim3((uint32_t)blocks), dim3(kThreads), 0, st, a, cols);
         if ((rc = hipGetLastError()) != hipSuccess) return rc;
-        if (a.d_bias && splits > 1) {
-            hipLaunchKernelGGL(k_expert_bias_sum, dim3(ceil_div(a.Nw, kThreads), a.E), dim3(kThreads), 0, st, a, splits);
-            if ((rc = hipGetLastError()) != hipSuccess) return rc;
-        }
+    }
+    if (a.d_bias) {
+        hipLaunchKernelGGL(k_expert_bias_sum, dim3(ceil_div(a.Nw, kWave), a.E), dim3(kThreads), 0, st, a);
+        if ((rc = hipGetLastError()) != hipSuccess) return rc;
     }
     if (a.d_x && a.rows > 0 && (rc = run<kDx, false>(a, st)) != hipSuccess) return rc;
     return a.d_w ? run<kDw, false>(a, st) : rc;

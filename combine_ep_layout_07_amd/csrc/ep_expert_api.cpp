@@ -75,7 +75,7 @@ int ep_query_expert_sizes(const ep_expert_config_t *cfg, ep_expert_sizes_t *sz) 
     sz->bias = E * Nw * 4;
     sz->out = rows * cfg->out_features * 2;
     sz->pre = rows * Nw * 2;
-    if (!fp8) sz->backward_scratch = grad_bytes(cfg) + E * ep::kActSplits * Nw * 4;
+    if (!fp8) sz->backward_scratch = grad_bytes(cfg) + ep::expert_row_tiles(rows, (int)E, ep::kActRows) * Nw * 4;
     return EP_OK;
 }
 
@@ -117,6 +117,7 @@ int ep_expert_mm_backward(const ep_expert_config_t *cfg, const int32_t *expert_b
     a.d_out = static_cast<const uint16_t *>(d_out_dev);
     a.d = static_cast<uint16_t *>(scratch_dev);
     a.part = reinterpret_cast<float *>(static_cast<char *>(scratch_dev) + grad_bytes(cfg));
+    a.part_tiles = ep::expert_row_tiles(a.rows, a.E, ep::kActRows);
     a.d_x = static_cast<uint16_t *>(d_x_dev);
     a.d_w = static_cast<uint16_t *>(d_w_dev);
     a.d_bias = d_bias_dev;

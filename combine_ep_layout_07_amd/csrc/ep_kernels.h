@@ -146,10 +146,9 @@ struct CombineBackwardArgs {
     float *d_topk_weights;   // null: not wanted
 };
 
-// Blocks of the router's forward pass over all sources, at most (each leaves
-// partial sums for the balance loss).
-constexpr int kRouteMaxBlocks = 1024;
-int route_blocks(int S, int T);
+// Blocks per source of the router's forward pass with the balance loss; each
+// leaves partial sums.
+int route_blocks(int S, int T, int E);
 
 struct RouteArgs {
     int S, T, E, K;
@@ -163,8 +162,9 @@ struct RouteArgs {
     float *topk_weights;
     int32_t *tokens_per_expert, *tokens_valid;
     float *balance_loss;
-    float *part_p;       // scratch [S*B][E]: sums of p; null without a balance loss
-    int32_t *part_cnt;   // scratch [S*B][E]: chosen lanes
+    int pitch;           // E rounded up to 4
+    float *part_p;       // scratch [S*B][pitch]: sums of p; null without a balance loss
+    int32_t *part_cnt;   // scratch [S*B][pitch]: chosen lanes
     int32_t *part_seen;  // scratch [S*B]: valid tokens
     const float *d_weights, *d_loss;  // backward; either may be null
     void *d_logits;

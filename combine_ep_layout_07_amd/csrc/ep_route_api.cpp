@@ -27,8 +27,10 @@ int check_config(const ep_route_config_t *c) {
 }
 
 uint64_t units(const ep_route_config_t *c) {
-    return (uint64_t)c->num_src_ranks * ep::route_blocks(c->num_src_ranks, c->num_tokens);
+    return (uint64_t)c->num_src_ranks * ep::route_blocks(c->num_src_ranks, c->num_tokens, c->num_experts);
 }
+
+int pitch(const ep_route_config_t *c) { return (c->num_experts + 3) / 4 * 4; }
 
 // Shape and tables common to both directions.
 int make_args(const ep_route_config_t *c, const void *logits_dev, const uint8_t *token_mask_dev,
@@ -41,7 +43,7 @@ int make_args(const ep_route_config_t *c, const void *logits_dev, const uint8_t 
     if (tok && (!logits_dev || !aligned(logits_dev, el) || !r->topk_idx_dev || !aligned(r->topk_idx_dev, 8)))
         return EP_ERR_INVALID_ARG;
     if (!aligned(r->topk_weights_dev, 4) || !aligned(r->tokens_per_expert_dev, 4) || !aligned(r->tokens_valid_dev, 4) ||
-        !aligned(r->balance_loss_dev, 4) || !aligned(r->scratch_dev, 8))
+        !aligned(r->balance_loss_dev, 4) || !aligned(r->scratch_dev, 16))
         return EP_ERR_INVALID_ARG;
     ep::RouteArgs &a = *out;
     memset(&a, 0, sizeof(a));
@@ -49,6 +51,7 @@ int make_args(const ep_route_config_t *c, const void *logits_dev, const uint8_t 
     a.T = c->num_tokens;
     a.E = c->num_experts;
     a.K = c->num_topk;
+    a.pitch = pitch(c);
     a.logits_bf16 = c->logits_dtype == EP_DTYPE_BF16;
     a.sigmoid = c->scoring == EP_SCORING_SIGMOID;
     a.scale = c->scale;
@@ -78,7 +81,7 @@ int ep_query_route_sizes(const ep_route_config_t *cfg, ep_route_sizes_t *sz) {
     sz->tokens_per_expert = S * E * sizeof(int32_t);
     sz->tokens_valid = S * sizeof(int32_t);
     sz->balance_loss = S * sizeof(float);
-    sz->scratch = units(cfg) * (2 * E + 1) * 4;
+    sz->scratch = units(cfg) * (2 * pitch(cfg) + 1) * 4;
     return EP_OK;
 }
 
@@ -92,7 +95,7 @@ int ep_route(const ep_route_config_t *cfg, const void *logits_dev, const float *
     if (given != 0 && given != 4) return EP_ERR_INVALID_ARG;
     a.bias = bias_dev;
     if (given) {
-        const uint64_t words = units(cfg) * (uint64_t)a.E;
+        const uint64_t words = units(cfg) * (uint64_t)a.pitch;
         a.part_p = static_cast<float *>(route->scratch_dev);
         a.part_cnt = reinterpret_cast<int32_t *>(a.part_p + words);
         a.part_seen = a.part_cnt + words;

@@ -373,7 +373,7 @@ typedef struct ep_route_sizes {
  *                     f_e = tokens_per_expert[e] * E / (K * max(V, 1)) and
  *                     P_e = sum over tokens of p_e / max(V, 1); p = s (softmax)
  *                     or s / (sum of the token's s + 1e-20) (sigmoid)
- *   scratch           8-byte aligned, private to the library, needs no
+ *   scratch           16-byte aligned, private to the library, needs no
  *                     initialisation */
 typedef struct ep_route {
     int64_t *topk_idx_dev;
