@@ -9,7 +9,7 @@ enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
 
 // Rows of a tile of the activation's backward pass (each leaves one partial sum
 // per column for d_bias).
-constexpr int kActRows = 64;
+constexpr int kActRows = 16;
 
 // Tiles of `size` rows that E segments of `rows` rows in all can make, at most.
 inline int64_t expert_row_tiles(int64_t rows, int E, int size) { return rows / size + (rows < E ? rows : E); }
@@ -47,6 +47,24 @@ __device__ __forceinline__ Segment segment_of(const int32_t *base, int e, int64_
     return {e, a, (int)(b - a)};
 }
 
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, kRowShr1, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, kRowShr2, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, kRowShr4, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, kRowShr8, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, kRowBcast15, 0xa, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, kRowBcast31, 0xc, 0xf, false);
+    return v;
+}
+
+// All tiles of `size` rows of the first E experts' segments.
+__device__ __forceinline__ int count_tiles(const int32_t *base, int E, int64_t rows, int size) {
+    int n = 0;
+    for (int e = lane_id(); e < E; e += kWave) n += (segment_of(base, e, rows).n + size - 1) / size;
+    return read_lane(wave_scan(n), kWave - 1);
+}
+
 // Tile `tile` of `size` rows, counted over the experts in order: a scan over
 // the experts by the whole wave, 64 at a time.
 __device__ __forceinline__ Segment find_tile(const int32_t *base, int E, int64_t rows, int size, int64_t tile) {
@@ -56,12 +74,7 @@ __device__ __forceinline__ Segment find_tile(const int32_t *base, int E, int64_t
         const int e = e0 + lane;
         const Segment g = e < E ? segment_of(base, e, rows) : Segment{e, 0, 0};
         const int mine = (g.n + size - 1) / size;
-        int incl = mine;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int v = shfl(incl, lane - d < 0 ? lane : lane - d);
-            if (lane >= d) incl += v;
-        }
+        const int incl = wave_scan(mine);
         const uint64_t past = ballot(before + incl > tile);
         if (past) {
             const int o = __builtin_ctzll(past);

@@ -19,46 +19,27 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 enum { kForward = 0, kDx = 1, kDw = 2 };
 
-// Bias, activation and residual of four neighbouring outputs, from the fp32
-// sums `v` (and, gated, the up projection's).
-__device__ __forceinline__ void finish(const ExpertArgs &a, int e, int64_t r, int c, f32x4 v, f32x4 up) {
-    const bool gated = a.act == kActSwiglu;
-    const int64_t b = (int64_t)e * a.Nw + c;
-    if (a.bias) {
-        v += *reinterpret_cast<const f32x4 *>(a.bias + b);
-        if (gated) up += *reinterpret_cast<const f32x4 *>(a.bias + b + a.N);
-    }
-    if (a.pre) {
-        uint16_t *to = a.pre + r * a.Nw + c;
-        *reinterpret_cast<u32x2 *>(to) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-        if (gated) *reinterpret_cast<u32x2 *>(to + a.N) = u32x2{pack_bf16(up[0], up[1]), pack_bf16(up[2], up[3])};
-    }
-    u32x2 res = {0u, 0u};
-    if (a.residual) res = *reinterpret_cast<const u32x2 *>(a.residual + r * a.N + c);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = gated ? v[i] * logistic(v[i]) * up[i] : activate(a.act, v[i]);
-        if (a.residual) v[i] += i % 2 ? bf16_hi(res[i / 2]) : bf16_lo(res[i / 2]);
-    }
-    *reinterpret_cast<u32x2 *>(a.out + r * a.N + c) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-}
-
 // ---- The tiled product ----
 //
-// A tile of BQ rows x BP columns by WQ x WP waves.  A step of the sum is 128
-// bytes of k (64 bf16, 128 fp8) of both operands: the DMA path writes them to
-// LDS (16 bytes a lane, no registers), one step ahead of the matrix units, in
-// two stages.  D comes transposed from the matrix unit (its rows are P's
-// columns), so that a lane holds four neighbours of a row of the output.
+// A tile of BQ rows x BP columns by WQ x WP waves.  The sum runs in steps of SB
+// bytes of k (64 bytes: 32 bf16); the DMA path writes both operands of a step to
+// one of NST stages of LDS (16 bytes a lane, no registers), NST - 1 steps ahead
+// of the matrix unit.  D comes transposed from the matrix unit (its rows are
+// P's columns), so that a lane holds four neighbours of a row of the output.
 //
-// An operand contiguous in k lies in LDS as rows of 128 bytes, chunk c of row r
-// at slot c ^ (r & 7).  One contiguous across k lies as 64 rows of k, the
-// 32-byte unit u of row k at u ^ ((k & 3) | (k & 8) >> 1), and is read by the
-// transposing LDS load.  Both place every read's lanes in different banks; the
-// permutation is made by each lane's global address, since the DMA writes a
-// wave's 1 KiB in lane order.
+// An operand contiguous in k lies in LDS as rows of SB bytes, chunk c (16 bytes)
+// of row r at slot c ^ (r & 7) (SB 128) or c ^ (r / 2 & 3) (SB 64).  One
+// contiguous across k lies as rows of k, the 32-byte unit u of row k at
+// u ^ ((k & 3) | (k & 8) >> 1), and is read by the transposing LDS load.  Both
+// place the lanes of every read in different banks; the permutation is made by
+// each lane's global address, since the DMA writes a wave's 1 KiB in lane order.
 constexpr uint32_t kOutside = 0x80000000u;  // past every buffer: the load returns zeros
 
+// s_waitcnt: at most `vm` loads and `lds` LDS operations outstanding.
+constexpr int wait_for(int vm, int lds) { return (vm & 15) | (vm >> 4) << 14 | 7 << 4 | lds << 8; }
+constexpr int kAnyLds = 15, kAnyLoads = 63;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
@@ -69,28 +50,33 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 }
 
 // One operand's part of a stage, of B rows (ALONG k) or B columns.
-template <bool ALONG, int B, int NW>
+template <bool ALONG, int B, int NW, int SB>
 struct Loader {
-    static constexpr int kLoads = B / 8 / NW;         // of 1 KiB, per wave
-    static constexpr int kLanes = ALONG ? 8 : B / 8;  // lanes of one row
-    static constexpr int kRows = kWave / kLanes;      // rows of one load
+    static constexpr int kLoads = B * SB / 1024 / NW;       // of 1 KiB, per wave
+    static constexpr int kLanes = ALONG ? SB / 16 : B / 8;  // lanes of one row
+    static constexpr int kRows = kWave / kLanes;            // rows of one load
+    static constexpr int kFull = ALONG ? SB / 16 : SB / 2;  // chunks or rows of k of a whole step
     const char *at;
     int64_t step;
-    uint32_t off[kLoads];
-    int place;  // ALONG: the lane's chunk; else its k row in the wave's first load
+    uint32_t off;    // of the wave's first load; kOutside: the lane's column does not exist
+    uint32_t apart;  // bytes between the wave's loads
+    uint32_t bytes;  // rows at or past the tile's end lie outside
+    int place;       // ALONG: the lane's chunk; else its k row in the wave's first load
 
     __device__ __forceinline__ static int row(int j, int wave, int lane) { return (j * NW + wave) * kRows + lane / kLanes; }
     __device__ __forceinline__ static int chunk(int r, int lane) {
-        return ALONG ? (lane % 8) ^ (r & 7) : (lane % kLanes) ^ (((r & 3) | (r & 8) >> 1) << 1);
+        if (!ALONG) return (lane % kLanes) ^ (((r & 3) | (r & 8) >> 1) << 1);
+        return (lane % kLanes) ^ (SB == 128 ? r & 7 : r / 2 & 3);
     }
-    // Issues the loads of one stage; `left` chunks (ALONG) or rows of k remain.
+    // Issues the loads of one stage; `left` chunks (ALONG) or rows of k remain
+    // (none: zeros, so that every step has as many loads).
     __device__ __forceinline__ void issue(char *stage, int wave, int left) {
         const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), 0, 0x7fffffff, 0x00020000);
-        const bool whole = left >= (ALONG ? 8 : 64);
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(at), 0, bytes, 0x00020000);
+        const bool whole = left >= kFull;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            uint32_t o = off[j];
+            uint32_t o = off + j * apart;
             if (!whole && (ALONG ? place : place + j * NW * kRows) >= left) o = kOutside;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_char *)(stage + (j * NW + wave) * 1024), 16, o, 0, 0, 0);
         }
@@ -98,21 +84,23 @@ struct Loader {
     }
 };
 
-// The lane's share of a 16-wide fragment for 32 steps of k (bf16).
-template <bool ALONG, int B>
+// The lane's share of a 16-wide fragment: 16 bytes of k of its row, for 64 bytes
+// of k over the four lane groups.
+template <bool ALONG, int B, int SB>
 struct Reader {
-    int addr, swz;
+    int addr, swz;  // ALONG: addresses of the first and the second 64 bytes of k
     __device__ __forceinline__ void init(int first, int lane) {  // first: the wave's first row or column
         const int g = lane / 16, m = lane % 16;
         if (ALONG) {
-            addr = (first + m) * 128 + ((g ^ (m & 7)) * 16);
+            addr = (first + m) * SB + ((g ^ (SB == 128 ? m & 7 : m / 2 & 3)) * 16);
+            swz = addr ^ 64;
         } else {
             addr = (g * 8 + m / 4) * (2 * B) + m % 4 * 8;
             swz = (first / 16) ^ ((m / 4) | (g & 1) << 2);
         }
     }
     __device__ __forceinline__ bf16x8 read(const char *lds, int i, int kk) const {
-        if (ALONG) return *reinterpret_cast<const bf16x8 *>(lds + ((addr + i * 2048) ^ (kk * 64)));
+        if (ALONG) return *reinterpret_cast<const bf16x8 *>(lds + (kk ? swz : addr) + i * 16 * SB);
         const char *p = lds + addr + (swz ^ i) * 32 + kk * 64 * B;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 8 * B));
@@ -120,23 +108,16 @@ struct Reader {
     }
 };
 
-// All tiles of `size` rows of the experts' segments.
-__device__ __forceinline__ int count_tiles(const int32_t *base, int E, int64_t rows, int size) {
-    int n = 0;
-    for (int e = lane_id(); e < E; e += kWave) n += (segment_of(base, e, rows).n + size - 1) / size;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) n += shfl(n, lane_id() ^ d);
-    return uniform(n);
-}
-
-// Workgroups go round the 8 XCDs; each XCD takes a contiguous eighth of the
-// tiles, in groups of 8 rows of tiles walked column by column, so that the
-// tiles it works on together share their operands in its L2.
-constexpr int kXcds = 8, kGroup = 8;
+// Workgroups go round the 8 XCDs.  Of every 128 tiles in order each XCD takes 16
+// neighbours, 4 rows of tiles by 4 columns, which share their operands in its
+// L2, while all XCDs together stay within one or two experts: at 32768 rows,
+// 16 experts, 7168 to 2 x 2048 that took 1.71 ms, a contiguous eighth of all
+// tiles per XCD 1.86 ms (fewer L2 misses, but twice as many rows open in the
+// memory behind), tiles in launch order 1.77 ms.
+constexpr int kXcds = 8, kPatch = 16, kGroup = 4;
 __device__ __forceinline__ bool place_tile(int b, int rows, int cols, int &row, int &col) {
-    const int total = rows * cols, per = (total + kXcds - 1) / kXcds;
-    const int i = b % kXcds * per + b / kXcds;
-    if (b / kXcds >= per || i >= total) return false;
+    const int i = b / (kXcds * kPatch) * (kXcds * kPatch) + b % kXcds * kPatch + b / kXcds % kPatch;
+    if (i >= rows * cols) return false;
     const int first = i / (kGroup * cols) * kGroup, in = i % (kGroup * cols);
     const int high = rows - first < kGroup ? rows - first : kGroup;
     row = first + in % high;
@@ -144,26 +125,109 @@ __device__ __forceinline__ bool place_tile(int b, int rows, int cols, int &row, 
     return true;
 }
 
-template <int MODE, bool FP8, int BQ, int BP, int WQ, int WP>
+// The workgroup's tile of `size` rows of an expert's segment and its column.
+__device__ __forceinline__ bool locate(const ExpertArgs &a, int size, int cols, Segment &g, int &col) {
+    int row;
+    if (a.E > kWave) {
+        if (!place_tile(blockIdx.x, count_tiles(a.base, a.E, a.rows, size), cols, row, col)) return false;
+        g = find_tile(a.base, a.E, a.rows, size, row);
+        return g.e >= 0;
+    }
+    const int lane = lane_id();
+    g = lane < a.E ? segment_of(a.base, lane, a.rows) : Segment{lane, 0, 0};
+    const int mine = (g.n + size - 1) / size, incl = wave_scan(mine);
+    if (!place_tile(blockIdx.x, read_lane(incl, kWave - 1), cols, row, col)) return false;
+    const int o = __builtin_ctzll(ballot(incl > row));
+    const int at = row - (read_lane(incl, o) - read_lane(mine, o));
+    const int left = read_lane(g.n, o) - at * size;
+    g = {o, (int64_t)read_lane((int)g.r0, o) + (int64_t)at * size, left < size ? left : size};
+    return true;
+}
+
+// Bias, activation and residual of eight neighbouring outputs, from the fp32
+// sums `v` (and, gated, the up projection's).
+__device__ __forceinline__ void finish(const ExpertArgs &a, int e, int64_t r, int c, float (&v)[8], float (&up)[8]) {
+    const bool gated = a.act == kActSwiglu;
+    if (a.bias) {
+        const f32x4 *b = reinterpret_cast<const f32x4 *>(a.bias + (int64_t)e * a.Nw + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += b[i / 4][i % 4];
+        if (gated) {
+            b = reinterpret_cast<const f32x4 *>(a.bias + (int64_t)e * a.Nw + a.N + c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) up[i] += b[i / 4][i % 4];
+        }
+    }
+    u32x4 o;
+    if (a.pre) {
+        uint16_t *to = a.pre + r * a.Nw + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<u32x4 *>(to) = o;
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = pack_bf16(up[2 * i], up[2 * i + 1]);
+            *reinterpret_cast<u32x4 *>(to + a.N) = o;
+        }
+    }
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * logistic(v[i]) * up[i];
+    } else if (a.act != kActNone) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = activate(a.act, v[i]);
+    }
+    if (a.residual) {
+        const u32x4 res = *reinterpret_cast<const u32x4 *>(a.residual + r * a.N + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += i % 2 ? bf16_hi(res[i / 2]) : bf16_lo(res[i / 2]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<u32x4 *>(a.out + r * a.N + c) = o;
+}
+
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(wait_for(kAnyLoads, 0));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A lane's four sums: the matrix unit's own registers, or, for fp8, four that
+// stay apart (as a vector the compiler moved them at every step).
+struct Four {
+    float v[4];
+    __device__ __forceinline__ float &operator[](int i) { return v[i]; }
+};
+template <bool FP8>
+struct Sum {
+    typedef f32x4 type;
+};
+template <>
+struct Sum<true> {
+    typedef Four type;
+};
+
+template <int MODE, bool FP8, int BQ, int BP, int WQ, int WP, int SB, int NST>
 __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, int cols) {
     constexpr int NW = WQ * WP, NQ = BQ / WQ / 16, NP = BP / WP / 16;
     constexpr bool QA = MODE != kDw, PA = MODE == kForward;
-    constexpr int kStage = (BQ + BP) * 128;
-    __shared__ __align__(1024) char smem[2][kStage];
+    constexpr int kStage = (BQ + BP) * SB;
+    __shared__ __align__(1024) char smem[NST * kStage];
     const int lane = lane_id(), wave = uniform(threadIdx.x / kWave);
     const int wq = wave % WQ * (BQ / WQ), wp = wave / WQ * (BP / WP);
     const bool gated = MODE == kForward && a.act == kActSwiglu;
-    int trow, tcol, q0 = 0;
+    int tcol, q0 = 0;
     Segment g;
     if (MODE == kDw) {
         const int per = (a.Nw + BQ - 1) / BQ;
+        int trow;
         if (!place_tile(blockIdx.x, per * a.E, cols, trow, tcol)) return;
         g = segment_of(a.base, trow / per, a.rows);
         q0 = trow % per * BQ;
-    } else {
-        if (!place_tile(blockIdx.x, count_tiles(a.base, a.E, a.rows, BQ), cols, trow, tcol)) return;
-        g = find_tile(a.base, a.E, a.rows, BQ, trow);
-        if (g.e < 0) return;
+    } else if (!locate(a, BQ, cols, g, tcol)) {
+        return;
     }
     const int64_t r0 = uniform64(g.r0);
     const int e = uniform(g.e), n = uniform(g.n);
@@ -175,15 +239,16 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
     const int p0 = tcol * (gated ? BP / 2 : BP);
     const int nq = MODE == kDw ? min(a.Nw - q0, BQ) : n;
 
-    Loader<QA, BQ, NW> lq;
-    Loader<PA, BP, NW> lp;
+    Loader<QA, BQ, NW, SB> lq;
+    Loader<PA, BP, NW, SB> lp;
     const char *d = reinterpret_cast<const char *>(a.d), *x = static_cast<const char *>(a.x), *w = static_cast<const char *>(a.w);
     if (MODE == kForward) {
         lq.at = x + r0 * pitchx;
+        lp.at = w + (we + (int64_t)p0 * a.I) * EL;
         // Rows of the tile alternate between 16 of the gate and 16 of the up
-        // projection; a wave's loads all lie in one of the two.
-        const bool up = gated && wave / 2 % 2;
-        lp.at = w + (we + (int64_t)(p0 + (up ? a.N : 0)) * a.I) * EL;
+        // projection; all of a wave's loads lie in one of the two.
+        static_assert(MODE != kForward || NW * lp.kRows % 32 == 0, "a wave's loads keep their side");
+        if (gated && wave * lp.kRows / 16 % 2) lp.at += (int64_t)a.N * pitchx;
     } else if (MODE == kDx) {
         lq.at = d + r0 * pitchd;
         lp.at = w + (we + p0) * 2;
@@ -191,127 +256,276 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
         lq.at = d + r0 * pitchd + (int64_t)q0 * 2;
         lp.at = x + r0 * pitchx + (int64_t)p0 * 2;
     }
-    lq.step = QA ? 128 : 64 * pitchd;
-    lp.step = PA ? 128 : 64 * pitchx;
-#pragma unroll
-    for (int j = 0; j < lq.kLoads; ++j) {
-        const int r = lq.row(j, wave, lane), c = lq.chunk(r, lane);
-        const bool in = QA ? r < nq : c * 8 < nq;
-        lq.off[j] = in ? (uint32_t)(r * (QA && MODE == kForward ? pitchx : pitchd)) + c * 16 : kOutside;
-        if (j == 0) lq.place = QA ? c : r;
+    lq.step = QA ? SB : SB / 2 * pitchd;
+    lp.step = PA ? SB : SB / 2 * pitchx;
+    {
+        // Along k: the offsets grow with the row, so a bound at the end of the
+        // tile's last row turns the rows after it into zeros.  Across k: columns
+        // outside by the lane's offset, rows of k by `left`.
+        const int r = lq.row(0, wave, lane), c = lq.chunk(r, lane);
+        const uint32_t pitch = (uint32_t)(QA && MODE == kForward ? pitchx : pitchd);
+        lq.off = QA || c * 8 < nq ? r * pitch + c * 16 : kOutside;
+        lq.apart = NW * lq.kRows * pitch;
+        lq.bytes = QA ? (nq - 1) * pitch + SB : kOutside;
+        lq.place = QA ? c : r;
     }
-#pragma unroll
-    for (int j = 0; j < lp.kLoads; ++j) {
-        const int r = lp.row(j, wave, lane), c = lp.chunk(r, lane);
-        const int local = gated ? r / 32 * 16 + r % 16 : r;
-        const bool in = PA ? p0 + local < P : p0 + c * 8 < P;
-        lp.off[j] = in ? (uint32_t)(local * pitchx) + c * 16 : kOutside;
-        if (j == 0) lp.place = PA ? c : r;
+    {
+        const int r = lp.row(0, wave, lane), c = lp.chunk(r, lane);
+        const uint32_t pitch = (uint32_t)pitchx;
+        lp.off = PA || p0 + c * 8 < P ? (gated ? r / 32 * 16 + r % 16 : r) * pitch + c * 16 : kOutside;
+        lp.apart = NW * lp.kRows / (gated ? 2 : 1) * pitch;
+        lp.bytes = PA ? (min(P - p0, gated ? BP / 2 : BP) - 1) * pitch + SB : kOutside;
+        lp.place = PA ? c : r;
     }
-    Reader<QA, BQ> rq;
-    Reader<PA, BP> rp;
+    Reader<QA, BQ, SB> rq;
+    Reader<PA, BP, SB> rp;
     rq.init(wq, lane);
     rp.init(wp, lane);
 
-    f32x4 acc[NP][NQ];
+    typename Sum<FP8>::type acc[NP][NQ];
 #pragma unroll
     for (int i = 0; i < NP; ++i)
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
 
-    // fp8: places of the lane's scales
+    // fp8: the lane's scales of a step.  A wave's columns lie in one block of
+    // 128 weight rows, those of its up projection in two neighbours at most.
     const int nkb = a.I / 128;
-    const float *xs_at[FP8 ? NQ : 1], *ws_at[FP8 ? NP : 1];
-    float xs[FP8 ? NQ : 1], ws[FP8 ? NP : 1];
+    const float *xs_at = nullptr, *wg_at = nullptr;
+    int xs_off[FP8 ? NQ : 1], up_lo = 0, up_hi = 0, up_from = 0;
+    float xs[FP8 ? NQ : 1], wg = 0.0f, wl = 0.0f, wh = 0.0f;
     if (FP8) {
+        xs_at = a.x_sf + r0 * nkb;
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-            const int q = wq + j * 16 + lane % 16;
-            xs_at[j] = a.x_sf + (r0 + min(q, nq - 1)) * nkb;
+        for (int j = 0; j < NQ; ++j) xs_off[j] = min(wq + j * 16 + lane % 16, nq - 1) * nkb;
+        const int n0 = min(gated ? p0 + wp / 2 : p0 + wp, a.N - 1), blocks = (a.Nw + 127) / 128;
+        wg_at = a.w_sf + ((int64_t)e * blocks + n0 / 128) * nkb;
+        if (gated) {
+            const int lo = (a.N + n0) / 128;
+            up_lo = (lo - n0 / 128) * nkb;
+            up_hi = (min(lo + 1, blocks - 1) - n0 / 128) * nkb;
+            up_from = (lo + 1) * 128 - a.N - n0;  // columns from here on take the second
         }
+    }
+    auto scales = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int pl = wp + i * 16 + lane / 16 * 4;
-            const int c = min(gated ? p0 + pl / 32 * 16 + pl % 16 : p0 + pl, a.N - 1);
-            const int row = c + (gated && i % 2 ? a.N : 0);
-            ws_at[i] = a.w_sf + ((int64_t)e * ((a.Nw + 127) / 128) + row / 128) * nkb;
+        for (int j = 0; j < NQ; ++j) xs[j] = xs_at[xs_off[j] + t];
+        wg = wg_at[t];
+        if (gated) wl = wg_at[up_lo + t], wh = wg_at[up_hi + t];
+    };
+    auto scale_of = [&](int i) {
+        const float first = wg, lo = wl, hi = wh;
+        if (!gated || i % 2 == 0) return first;
+        return i / 2 * 16 + lane / 16 * 4 < up_from ? lo : hi;
+    };
+    auto both = [](bf16x8 lo, bf16x8 hi) {
+        return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    auto mfma8 = [](i32x8 p, i32x8 q) {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+    };
+    auto add_scaled = [](typename Sum<FP8>::type &c, f32x4 part, float sc) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) c[r] = fmaf(part[r], sc, c[r]);
+        // Here and not later: left to itself the compiler holds the products of
+        // a whole step until its end, which spills.
+        asm volatile("" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
+    };
+
+    constexpr int kPerStep = SB / EL, kIssued = lq.kLoads + lp.kLoads;
+    const int steps = (K + kPerStep - 1) / kPerStep;
+    auto issue = [&](int t, int stage) {
+        const int left = K - t * kPerStep;
+        char *to = smem + stage * kStage;
+        lq.issue(to, wave, QA ? left / (16 / EL) : left);
+        lp.issue(to + BQ * SB, wave, PA ? left / (16 / EL) : left);
+    };
+    auto next = [](int stage) { return stage + 1 == NST ? 0 : stage + 1; };
+    // The oldest step's loads are done when those of NST - 2 steps may be out.
+    constexpr int kLanded = (NST - 2) * kIssued;
+    static_assert(kLanded < kAnyLoads && (!FP8 || NST == 2), "the scales' loads are counted with the stage's");
+    if (steps > 0)
+        for (int t = 0; t < NST - 1; ++t) issue(t, t);
+    int rd = 0, wr = NST - 1;
+    if (NW == 8 && steps > 0) {
+        // Two waves on each SIMD, of the two halves of the workgroup: one reads
+        // its fragments while the other keeps the matrix unit, and at the next
+        // barrier they change places; the second half runs one turn behind,
+        // held by one barrier more at the start.  fp8 has four such turns per
+        // step (halves of P by halves of Q, in an order that reads one new half
+        // a turn; all fragments of a step would not fit the registers).  A stage is written again from the turn after the second
+        // half's last read of it on.  Each wave waits for its own loads in the
+        // last turn before the first half reads them.
+        constexpr int kTurns = FP8 ? 4 : 1;
+        static_assert(FP8 ? SB == 128 : SB == 64, "one turn's fragments");
+        const bool second = wave >= 4;
+        auto turn = [] {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
+        asm volatile("" ::: "memory");
+        turn();
+        if (second) turn();
+        for (int t = 0; t < steps; ++t) {
+            const char *sq = smem + rd * kStage, *sp = sq + BQ * SB;
+            i32x8 wideq[FP8 ? NQ / 2 : 1], widep[FP8 ? NP / 2 : 1];
+#pragma unroll
+            for (int h = 0; h < kTurns; ++h) {
+                const int q1 = (h == 1 || h == 2) * (NQ / 2), p1 = (h >= 2) * (NP / 2);
+                asm volatile("" ::: "memory");
+                bf16x8 fq[FP8 ? 1 : NQ], fp[FP8 ? 1 : NP];
+                if (FP8) {
+                    if (h == 0) scales(t);
+#pragma unroll
+                    for (int j = 0; j < NQ / 2 && h != 2; ++j) wideq[j] = both(rq.read(sq, q1 + j, 0), rq.read(sq, q1 + j, 1));
+#pragma unroll
+                    for (int i = 0; i < NP / 2 && h % 2 == 0; ++i) widep[i] = both(rp.read(sp, p1 + i, 0), rp.read(sp, p1 + i, 1));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) fq[j] = rq.read(sq, j, 0);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) fp[i] = rp.read(sp, i, 0);
+                }
+                if (h == 0) issue(t + NST - 1, wr);
+                asm volatile("" ::: "memory");
+                if (h == kTurns - 1 && second) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, 0));
+                else __builtin_amdgcn_s_waitcnt(wait_for(kAnyLoads, 0));
+                turn();
+                __builtin_amdgcn_s_setprio(1);
+                if constexpr (FP8) {
+                    // The products of column i and the scaling of column i - 1
+                    // overlap.
+                    f32x4 part[2][NQ / 2];
+#pragma unroll
+                    for (int i = 0; i <= NP / 2; ++i) {
+#pragma unroll
+                        for (int j = 0; j < NQ / 2 && i < NP / 2; ++j) part[i % 2][j] = mfma8(widep[i], wideq[j]);
+#pragma unroll
+                        for (int j = 0; j < NQ / 2 && i > 0; ++j)
+                            add_scaled(acc[p1 + i - 1][q1 + j], part[(i - 1) % 2][j], xs[q1 + j] * scale_of(p1 + i - 1));
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
+                }
+                __builtin_amdgcn_s_setprio(0);
+                asm volatile("" ::: "memory");
+                if (h == kTurns - 1 && !second) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
+                turn();
+            }
+            rd = next(rd);
+            wr = next(wr);
+        }
+        if (!second) turn();
+    } else {
+        for (int t = 0; t < steps; ++t) {
+            // The step's loads have landed, and every wave is done with the
+            // stage that is written next.
+            __builtin_amdgcn_s_waitcnt(wait_for(kLanded, 0));
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (FP8) scales(t);
+            issue(t + NST - 1, wr);
+            const char *sq = smem + rd * kStage, *sp = sq + BQ * SB;
+            if constexpr (!FP8) {
+#pragma unroll
+                for (int kk = 0; kk < SB / 64; ++kk) {
+                    bf16x8 fq[NQ], fp[NP];
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) fq[j] = rq.read(sq, j, kk);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) fp[i] = rp.read(sp, i, kk);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
+                }
+            } else {
+                i32x8 fq[NQ];
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) fq[j] = both(rq.read(sq, j, 0), rq.read(sq, j, 1));
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const i32x8 fp = both(rp.read(sp, i, 0), rp.read(sp, i, 1));
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j) add_scaled(acc[i][j], mfma8(fp, fq[j]), xs[j] * scale_of(i));
+                }
+            }
+            rd = next(rd);
+            wr = next(wr);
         }
     }
 
-    const int per_step = FP8 ? 128 : 64;
-    const int steps = (K + per_step - 1) / per_step;
-    auto issue = [&](int t, char *stage) {
-        const int left = K - t * per_step;
-        lq.issue(stage, wave, QA ? left / (16 / EL) : left);
-        lp.issue(stage + BQ * 128, wave, PA ? left / (16 / EL) : left);
-    };
-    if (steps > 0) issue(0, smem[0]);
-    for (int t = 0; t < steps; ++t) {
-        // The stage's loads have landed, and every wave is done with the other
-        // stage (its reads fed matrix operations that were issued before).
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (FP8) {
+    // The tile goes through LDS, so that rows leave in 16-byte pieces of whole
+    // lines (stored from the accumulators they leave as 8-byte pieces of 16
+    // rows: 12 us per 256 x 256 tile).  Forward: fp32, as many rows at a time
+    // as fit, and the epilogue in row order; gradients: already rounded.
+    __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
+    if (MODE == kForward) {
+        constexpr int kRowsPer = BQ < 128 ? BQ : 128;
+        static_assert(kRowsPer * BP * 4 <= NST * kStage, "LDS");
+        const int per = gated ? BP / 16 : BP / 8;
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) xs[j] = xs_at[j][t];
-#pragma unroll
-            for (int i = 0; i < NP; ++i) ws[i] = ws_at[i][t];
-        }
-        if (t + 1 < steps) issue(t + 1, smem[(t + 1) & 1]);
-        const char *sq = smem[t & 1], *sp = sq + BQ * 128;
-        if (!FP8) {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                bf16x8 fq[NQ], fp[NP];
-#pragma unroll
-                for (int j = 0; j < NQ; ++j) fq[j] = rq.read(sq, j, kk);
-#pragma unroll
-                for (int i = 0; i < NP; ++i) fp[i] = rp.read(sp, i, kk);
+        for (int h = 0; h < BQ / kRowsPer; ++h) {
+            lds_barrier();
+            if (wq / kRowsPer == h) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
 #pragma unroll
-                    for (int j = 0; j < NQ; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
+                    for (int j = 0; j < NQ; ++j) {
+                        const int q = wq % kRowsPer + j * 16 + lane % 16, c = (wp + i * 16) / 4 + lane / 16;
+                        *reinterpret_cast<f32x4 *>(smem + q * BP * 4 + (c ^ (q & 7)) * 16) =
+                            f32x4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                    }
             }
-        } else {
-            auto wide = [](bf16x8 lo, bf16x8 hi) {
-                typedef int i32x4 __attribute__((ext_vector_type(4)));
-                return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
-            };
-            i32x8 fq[NQ];
+            lds_barrier();
+            for (int it = threadIdx.x; it < kRowsPer * per; it += NW * kWave) {
+                const int q = it / per, c8 = it % per, c = p0 + c8 * 8;
+                if (h * kRowsPer + q >= nq || c >= a.N) continue;
+                const char *row = smem + q * BP * 4;
+                const int c4 = gated ? c8 / 2 * 8 + c8 % 2 * 2 : c8 * 2;
+                float v[8], up[8];
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) fq[j] = wide(rq.read(sq, j, 0), rq.read(sq, j, 1));
+                for (int k = 0; k < 2; ++k) {
+                    const f32x4 l = *reinterpret_cast<const f32x4 *>(row + ((c4 + k) ^ (q & 7)) * 16);
+                    f32x4 u = l;
+                    if (gated) u = *reinterpret_cast<const f32x4 *>(row + ((c4 + 4 + k) ^ (q & 7)) * 16);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const i32x8 fp = wide(rp.read(sp, i, 0), rp.read(sp, i, 1));
-#pragma unroll
-                for (int j = 0; j < NQ; ++j) {
-                    const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        fp, fq[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-                    const float sc = xs[j] * ws[i];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(part[r], sc, acc[i][j][r]);
+                    for (int i = 0; i < 4; ++i) v[4 * k + i] = l[i], up[4 * k + i] = u[i];
                 }
+                finish(a, e, r0 + h * kRowsPer + q, c, v, up);
             }
         }
-    }
+    } else {
+        static_assert(MODE == kForward || BQ * BP * 2 <= NST * kStage, "LDS");
+        lds_barrier();
 #pragma unroll
-    for (int i = 0; i < NP; ++i)
+        for (int i = 0; i < NP; ++i)
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-            const int q = wq + j * 16 + lane % 16, pl = wp + i * 16 + lane / 16 * 4;
-            if (q >= nq) continue;
-            if (MODE == kForward) {
-                if (gated && i % 2) continue;
-                const int c = gated ? p0 + pl / 32 * 16 + pl % 16 : p0 + pl;
-                if (c < a.N) finish(a, e, r0 + q, c, acc[i][j], acc[i | 1][j]);
-            } else if (p0 + pl < P) {
-                uint16_t *dst = MODE == kDx ? a.d_x + (r0 + q) * a.I : a.d_w + we + (int64_t)(q0 + q) * a.I;
-                *reinterpret_cast<u32x2 *>(dst + p0 + pl) =
+            for (int j = 0; j < NQ; ++j) {
+                const int q = wq + j * 16 + lane % 16, p = wp + i * 16 + lane / 16 * 4;
+                *reinterpret_cast<u32x2 *>(smem + q * BP * 2 + (p / 8 ^ (q & 15)) * 16 + p % 8 * 2) =
                     u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
             }
+        lds_barrier();
+        uint16_t *to = MODE == kDx ? a.d_x + r0 * a.I : a.d_w + we + (int64_t)q0 * a.I;
+        for (int it = threadIdx.x; it < BQ * BP / 8; it += NW * kWave) {
+            const int q = it / (BP / 8), c = it % (BP / 8);
+            if (q < nq && p0 + c * 8 < P)
+                *reinterpret_cast<u32x4 *>(to + (int64_t)q * a.I + p0 + c * 8) =
+                    *reinterpret_cast<const u32x4 *>(smem + q * BP * 2 + (c ^ (q & 15)) * 16);
         }
+    }
 }
 
 // Gradient of the pre-activation, bf16, and the columns' sums of its unrounded
@@ -407,7 +621,7 @@ __global__ void __launch_bounds__(kThreads) k_expert_bias_sum(ExpertArgs a) {
     const int last = (int)min((int64_t)first + tiles, a.part_tiles);
     float s = 0.0f;
     if (n < a.Nw) {
-#pragma unroll 4
+#pragma unroll 8
         for (int t = first + wave; t < last; t += kThreads / kWave) s += a.part[(int64_t)t * a.Nw + n];
     }
     sum[wave][lane] = s;
@@ -421,23 +635,23 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int64_t row_tiles(const ExpertArgs &a, int size) { return expert_row_tiles(a.rows, a.E, size); }
 
-template <int MODE, bool FP8, int BQ, int BP, int WQ, int WP>
+template <int MODE, bool FP8, int BQ, int BP, int WQ, int WP, int SB, int NST>
 hipError_t run_tile(const ExpertArgs &a, hipStream_t st) {
     const bool gated = MODE == kForward && a.act == kActSwiglu;
     const int64_t cols = ceil_div(MODE == kForward ? a.N : a.I, gated ? BP / 2 : BP);
     const int64_t tiles = MODE == kDw ? (int64_t)ceil_div(a.Nw, BQ) * a.E : row_tiles(a, BQ);
-    const int64_t blocks = (tiles * cols + kXcds - 1) / kXcds * kXcds;
+    const int64_t blocks = (tiles * cols + kXcds * kPatch - 1) / (kXcds * kPatch) * (kXcds * kPatch);
     if (blocks > 4294967295ll / (WQ * WP * kWave)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_expert_tile<MODE, FP8, BQ, BP, WQ, WP>), dim3((uint32_t)blocks), dim3(WQ * WP * kWave), 0, st,
-                       a, (int)cols);
+    hipLaunchKernelGGL((k_expert_tile<MODE, FP8, BQ, BP, WQ, WP, SB, NST>), dim3((uint32_t)blocks), dim3(WQ * WP * kWave),
+                       0, st, a, (int)cols);
     return hipGetLastError();
 }
 
 template <int MODE, bool FP8>
 hipError_t run(const ExpertArgs &a, hipStream_t st) {
     const int64_t each = MODE == kDw ? a.Nw : a.rows / a.E;
-    if (each >= 256) return run_tile<MODE, FP8, 256, 256, 4, 2>(a, st);
-    return run_tile<MODE, FP8, 128, 128, 2, 2>(a, st);
+    if (each >= 256) return run_tile<MODE, FP8, 256, 256, 4, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
+    return run_tile<MODE, FP8, 128, 128, 2, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
 }
 
 }  // namespace
