@@ -290,36 +290,45 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
 
-    // fp8: the lane's scales of a step.  A wave's columns lie in one block of
-    // 128 weight rows, those of its up projection in two neighbours at most.
+    // fp8: the scales of eight steps at a time go to LDS, [row][8] for x, and
+    // for the weights the tile's two or three blocks of 128 weight rows: its
+    // columns', or gated the gate's one and the up projection's two at most.
+    // (Loaded by each lane at each step they took a third of the time: a line
+    // for every row, every time anew.)
+    constexpr int kBlocks = 8;
+    __shared__ float sxs[FP8 ? 2 : 1][FP8 ? BQ * kBlocks : 1], sws[FP8 ? 2 : 1][FP8 ? kWave : 1];
     const int nkb = a.I / 128;
-    const float *xs_at = nullptr, *wg_at = nullptr;
-    int xs_off[FP8 ? NQ : 1], up_lo = 0, up_hi = 0, up_from = 0;
-    float xs[FP8 ? NQ : 1], wg = 0.0f, wl = 0.0f, wh = 0.0f;
-    if (FP8) {
-        xs_at = a.x_sf + r0 * nkb;
+    const int up_from = ((a.N + p0) / 128 + 1) * 128 - a.N - p0 - wp / 2;  // the wave's columns from here on take the third
+    auto load_scales = [&](int kb0) {
+        const int to = kb0 / kBlocks % 2, kb = kb0 + lane % kBlocks;
+        const __amdgpu_buffer_rsrc_t rx =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(a.x_sf + r0 * nkb), 0, kOutside, 0x00020000);
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) xs_off[j] = min(wq + j * 16 + lane % 16, nq - 1) * nkb;
-        const int n0 = min(gated ? p0 + wp / 2 : p0 + wp, a.N - 1), blocks = (a.Nw + 127) / 128;
-        wg_at = a.w_sf + ((int64_t)e * blocks + n0 / 128) * nkb;
-        if (gated) {
-            const int lo = (a.N + n0) / 128;
-            up_lo = (lo - n0 / 128) * nkb;
-            up_hi = (min(lo + 1, blocks - 1) - n0 / 128) * nkb;
-            up_from = (lo + 1) * 128 - a.N - n0;  // columns from here on take the second
+        for (int j = 0; j < BQ * kBlocks / kWave / NW; ++j) {
+            const int row = (j * NW + wave) * (kWave / kBlocks) + lane / kBlocks;
+            const uint32_t o = row < nq && kb < nkb ? (row * nkb + kb) * 4 : kOutside;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char *)&sxs[to][(j * NW + wave) * kWave], 4, o, 0, 0, 0);
         }
-    }
-    auto scales = [&](int t) {
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) xs[j] = xs_at[xs_off[j] + t];
-        wg = wg_at[t];
-        if (gated) wl = wg_at[up_lo + t], wh = wg_at[up_hi + t];
+        if (wave == 0) {
+            const int blocks = (a.Nw + 127) / 128, slot = lane / kBlocks;
+            const int block = gated && slot > 0 ? (a.N + p0) / 128 + slot - 1 : p0 / 128 + slot;
+            const uint32_t o = slot < 3 && block < blocks && kb < nkb ? (block * nkb + kb) * 4 : kOutside;
+            const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<float *>(a.w_sf + (int64_t)e * blocks * nkb), 0, kOutside, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_char *)&sws[to][0], 4, o, 0, 0, 0);
+        }
     };
-    auto scale_of = [&](int i) {
-        const float first = wg, lo = wl, hi = wh;
-        if (!gated || i % 2 == 0) return first;
-        return i / 2 * 16 + lane / 16 * 4 < up_from ? lo : hi;
+    auto x_scale = [&](int t, int j) {
+        return sxs[t / kBlocks % 2][(wq + j * 16 + lane % 16) * kBlocks + t % kBlocks];
     };
+    // The scales of even and of odd 16 columns of the wave, the latter up to
+    // and from up_from on.
+    auto w_scales = [&](int t) {
+        const float *s = &sws[t / kBlocks % 2][t % kBlocks];
+        const float first = s[gated ? 0 : wp / 128 * kBlocks], lo = s[kBlocks], hi = s[2 * kBlocks];
+        return f32x4{first, gated ? lo : first, gated ? hi : first, 0.0f};
+    };
+    auto w_scale = [&](f32x4 s, int i) { return i % 2 == 0 ? s[0] : (i / 2 * 16 + lane / 16 * 4 < up_from ? s[1] : s[2]); };
     auto both = [](bf16x8 lo, bf16x8 hi) {
         return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
     };
@@ -337,6 +346,7 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
     constexpr int kPerStep = SB / EL, kIssued = lq.kLoads + lp.kLoads;
     const int steps = (K + kPerStep - 1) / kPerStep;
     auto issue = [&](int t, int stage) {
+        if (FP8 && t % kBlocks == 0 && t < steps) load_scales(t);
         const int left = K - t * kPerStep;
         char *to = smem + stage * kStage;
         lq.issue(to, wave, QA ? left / (16 / EL) : left);
@@ -353,12 +363,12 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
         // Two waves on each SIMD, of the two halves of the workgroup: one reads
         // its fragments while the other keeps the matrix unit, and at the next
         // barrier they change places; the second half runs one turn behind,
-        // held by one barrier more at the start.  fp8 has four such turns per
-        // step (halves of P by halves of Q, in an order that reads one new half
-        // a turn; all fragments of a step would not fit the registers).  A stage is written again from the turn after the second
+        // held by one barrier more at the start.  fp8 has two such turns per
+        // step (the halves of P; all fragments of a step would not fit the
+        // registers).  A stage is written again from the turn after the second
         // half's last read of it on.  Each wave waits for its own loads in the
         // last turn before the first half reads them.
-        constexpr int kTurns = FP8 ? 4 : 1;
+        constexpr int kTurns = FP8 ? 2 : 1;
         static_assert(FP8 ? SB == 128 : SB == 64, "one turn's fragments");
         const bool second = wave >= 4;
         auto turn = [] {
@@ -372,18 +382,25 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
         if (second) turn();
         for (int t = 0; t < steps; ++t) {
             const char *sq = smem + rd * kStage, *sp = sq + BQ * SB;
-            i32x8 wideq[FP8 ? NQ / 2 : 1], widep[FP8 ? NP / 2 : 1];
+            i32x8 wideq[FP8 ? NQ : 1], widep[FP8 ? NP / 2 : 1];
+            float xs[FP8 ? NQ : 1];
+            f32x4 ws;
 #pragma unroll
             for (int h = 0; h < kTurns; ++h) {
-                const int q1 = (h == 1 || h == 2) * (NQ / 2), p1 = (h >= 2) * (NP / 2);
+                const int p1 = h * (NP / 2);
                 asm volatile("" ::: "memory");
                 bf16x8 fq[FP8 ? 1 : NQ], fp[FP8 ? 1 : NP];
                 if (FP8) {
-                    if (h == 0) scales(t);
+                    if (h == 0) {
+                        ws = w_scales(t);
 #pragma unroll
-                    for (int j = 0; j < NQ / 2 && h != 2; ++j) wideq[j] = both(rq.read(sq, q1 + j, 0), rq.read(sq, q1 + j, 1));
+                        for (int j = 0; j < NQ; ++j) {
+                            xs[j] = x_scale(t, j);
+                            wideq[j] = both(rq.read(sq, j, 0), rq.read(sq, j, 1));
+                        }
+                    }
 #pragma unroll
-                    for (int i = 0; i < NP / 2 && h % 2 == 0; ++i) widep[i] = both(rp.read(sp, p1 + i, 0), rp.read(sp, p1 + i, 1));
+                    for (int i = 0; i < NP / 2; ++i) widep[i] = both(rp.read(sp, p1 + i, 0), rp.read(sp, p1 + i, 1));
                 } else {
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) fq[j] = rq.read(sq, j, 0);
@@ -397,16 +414,19 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
                 turn();
                 __builtin_amdgcn_s_setprio(1);
                 if constexpr (FP8) {
-                    // The products of column i and the scaling of column i - 1
-                    // overlap.
-                    f32x4 part[2][NQ / 2];
+                    // Two products, and the scaling of the two before, at a time.
+                    constexpr int kPairs = NP / 2 * NQ / 2;
+                    f32x4 part[2][2];
 #pragma unroll
-                    for (int i = 0; i <= NP / 2; ++i) {
+                    for (int u = 0; u <= kPairs; ++u) {
 #pragma unroll
-                        for (int j = 0; j < NQ / 2 && i < NP / 2; ++j) part[i % 2][j] = mfma8(widep[i], wideq[j]);
+                        for (int v = 0; v < 2 && u < kPairs; ++v)
+                            part[u % 2][v] = mfma8(widep[u * 2 / NQ], wideq[u * 2 % NQ + v]);
 #pragma unroll
-                        for (int j = 0; j < NQ / 2 && i > 0; ++j)
-                            add_scaled(acc[p1 + i - 1][q1 + j], part[(i - 1) % 2][j], xs[q1 + j] * scale_of(p1 + i - 1));
+                        for (int v = 0; v < 2 && u > 0; ++v) {
+                            const int i = p1 + (u - 1) * 2 / NQ, j = (u - 1) * 2 % NQ + v;
+                            add_scaled(acc[i][j], part[(u - 1) % 2][v], xs[j] * w_scale(ws, i));
+                        }
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 } else {
@@ -433,7 +453,6 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            if (FP8) scales(t);
             issue(t + NST - 1, wr);
             const char *sq = smem + rd * kStage, *sp = sq + BQ * SB;
             if constexpr (!FP8) {
@@ -452,13 +471,15 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
                 }
             } else {
                 i32x8 fq[NQ];
+                float xs[NQ];
+                const f32x4 ws = w_scales(t);
 #pragma unroll
-                for (int j = 0; j < NQ; ++j) fq[j] = both(rq.read(sq, j, 0), rq.read(sq, j, 1));
+                for (int j = 0; j < NQ; ++j) xs[j] = x_scale(t, j), fq[j] = both(rq.read(sq, j, 0), rq.read(sq, j, 1));
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const i32x8 fp = both(rp.read(sp, i, 0), rp.read(sp, i, 1));
 #pragma unroll
-                    for (int j = 0; j < NQ; ++j) add_scaled(acc[i][j], mfma8(fp, fq[j]), xs[j] * scale_of(i));
+                    for (int j = 0; j < NQ; ++j) add_scaled(acc[i][j], mfma8(fp, fq[j]), xs[j] * w_scale(ws, i));
                 }
             }
             rd = next(rd);
