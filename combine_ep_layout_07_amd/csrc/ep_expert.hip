@@ -144,47 +144,45 @@ __device__ __forceinline__ bool locate(const ExpertArgs &a, int size, int cols, 
     return true;
 }
 
-// Bias, activation and residual of eight neighbouring outputs, from the fp32
-// sums `v` (and, gated, the up projection's).
-__device__ __forceinline__ void finish(const ExpertArgs &a, int e, int64_t r, int c, float (&v)[8], float (&up)[8]) {
-    const bool gated = a.act == kActSwiglu;
-    if (a.bias) {
-        const f32x4 *b = reinterpret_cast<const f32x4 *>(a.bias + (int64_t)e * a.Nw + c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += b[i / 4][i % 4];
-        if (gated) {
-            b = reinterpret_cast<const f32x4 *>(a.bias + (int64_t)e * a.Nw + a.N + c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) up[i] += b[i / 4][i % 4];
-        }
-    }
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
     u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    return o;
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const f32x4 lo = reinterpret_cast<const f32x4 *>(p)[0], hi = reinterpret_cast<const f32x4 *>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+}
+
+// Eight neighbouring outputs from the biased fp32 sums `v` (and, gated, those
+// of the up projection): the kept pre-activation, activation and residual.
+template <bool GATED>
+__device__ __forceinline__ void finish(const ExpertArgs &a, int64_t r, int c, float (&v)[8], const float (&up)[8], u32x4 res) {
     if (a.pre) {
         uint16_t *to = a.pre + r * a.Nw + c;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<u32x4 *>(to) = o;
-        if (gated) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = pack_bf16(up[2 * i], up[2 * i + 1]);
-            *reinterpret_cast<u32x4 *>(to + a.N) = o;
-        }
+        *reinterpret_cast<u32x4 *>(to) = pack8(v);
+        if (GATED) *reinterpret_cast<u32x4 *>(to + a.N) = pack8(up);
     }
-    if (gated) {
+    if (GATED) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] * logistic(v[i]) * up[i];
-    } else if (a.act != kActNone) {
+    } else if (a.act == kActGelu) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate(a.act, v[i]);
+        for (int i = 0; i < 8; ++i) v[i] = activate(kActGelu, v[i]);
+    } else if (a.act == kActSilu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = activate(kActSilu, v[i]);
+    } else if (a.act == kActRelu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = activate(kActRelu, v[i]);
     }
     if (a.residual) {
-        const u32x4 res = *reinterpret_cast<const u32x4 *>(a.residual + r * a.N + c);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += i % 2 ? bf16_hi(res[i / 2]) : bf16_lo(res[i / 2]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<u32x4 *>(a.out + r * a.N + c) = o;
+    *reinterpret_cast<u32x4 *>(a.out + r * a.N + c) = pack8(v);
 }
 
 __device__ __forceinline__ void lds_barrier() {
@@ -192,6 +190,64 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+}
+
+// The forward tile through LDS in fp32, as many rows at a time as fit, and the
+// epilogue in row order: a thread keeps its eight columns, so their bias is
+// loaded once, and has the residual of all its rows in flight before the sums
+// are in LDS (loaded row by row the epilogue took half of a small product).
+template <bool GATED, int BQ, int BP, int NW, int NP, int NQ, typename ACC>
+__device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, ACC (&acc)[NP][NQ], int e, int64_t r0, int p0,
+                                             int nq, int wq, int wp, int lane) {
+    constexpr int kRowsPer = BQ < 128 ? BQ : 128, kPer = BP / (GATED ? 16 : 8);
+    constexpr int kApart = NW * kWave / kPer, kItems = kRowsPer / kApart;
+    const int c8 = threadIdx.x % kPer, q0 = threadIdx.x / kPer, c = p0 + c8 * 8;
+    const int c4 = GATED ? c8 / 2 * 8 + c8 % 2 * 2 : c8 * 2;
+    float bv[8], bu[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bv[i] = bu[i] = 0.0f;
+    if (a.bias && c < a.N) {
+        load8(a.bias + (int64_t)e * a.Nw + c, bv);
+        if (GATED) load8(a.bias + (int64_t)e * a.Nw + a.N + c, bu);
+    }
+#pragma unroll
+    for (int h = 0; h < BQ / kRowsPer; ++h) {
+        u32x4 res[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int q = h * kRowsPer + q0 + k * kApart;
+            res[k] = u32x4{0u, 0u, 0u, 0u};
+            if (a.residual && q < nq && c < a.N) res[k] = *reinterpret_cast<const u32x4 *>(a.residual + (r0 + q) * a.N + c);
+        }
+        lds_barrier();
+        if (wq / kRowsPer == h) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    const int q = wq % kRowsPer + j * 16 + lane % 16, at = (wp + i * 16) / 4 + lane / 16;
+                    *reinterpret_cast<f32x4 *>(smem + q * BP * 4 + (at ^ (q & 7)) * 16) =
+                        f32x4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            const int q = q0 + k * kApart;
+            if (h * kRowsPer + q >= nq || c >= a.N) continue;
+            const char *row = smem + q * BP * 4;
+            float v[8], up[8];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x4 l = *reinterpret_cast<const f32x4 *>(row + ((c4 + i) ^ (q & 7)) * 16);
+                f32x4 u = l;
+                if (GATED) u = *reinterpret_cast<const f32x4 *>(row + ((c4 + 4 + i) ^ (q & 7)) * 16);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[4 * i + r] = l[r] + bv[4 * i + r], up[4 * i + r] = u[r] + bu[4 * i + r];
+            }
+            finish<GATED>(a, r0 + h * kRowsPer + q, c, v, up, res[k]);
+        }
+    }
 }
 
 // A lane's four sums: the matrix unit's own registers, or, for fp8, four that
@@ -369,7 +425,7 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
         // half's last read of it on.  Each wave waits for its own loads in the
         // last turn before the first half reads them.
         constexpr int kTurns = FP8 ? 2 : 1;
-        static_assert(FP8 ? SB == 128 : SB == 64, "one turn's fragments");
+        static_assert(NW != 8 || (FP8 ? SB == 128 : SB == 64), "one turn's fragments");
         const bool second = wave >= 4;
         auto turn = [] {
             __builtin_amdgcn_sched_barrier(0);
@@ -489,44 +545,12 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
 
     // The tile goes through LDS, so that rows leave in 16-byte pieces of whole
     // lines (stored from the accumulators they leave as 8-byte pieces of 16
-    // rows: 12 us per 256 x 256 tile).  Forward: fp32, as many rows at a time
-    // as fit, and the epilogue in row order; gradients: already rounded.
+    // rows: 12 us per 256 x 256 tile), gradients already rounded.
     __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
     if (MODE == kForward) {
-        constexpr int kRowsPer = BQ < 128 ? BQ : 128;
-        static_assert(kRowsPer * BP * 4 <= NST * kStage, "LDS");
-        const int per = gated ? BP / 16 : BP / 8;
-#pragma unroll
-        for (int h = 0; h < BQ / kRowsPer; ++h) {
-            lds_barrier();
-            if (wq / kRowsPer == h) {
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) {
-                        const int q = wq % kRowsPer + j * 16 + lane % 16, c = (wp + i * 16) / 4 + lane / 16;
-                        *reinterpret_cast<f32x4 *>(smem + q * BP * 4 + (c ^ (q & 7)) * 16) =
-                            f32x4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                    }
-            }
-            lds_barrier();
-            for (int it = threadIdx.x; it < kRowsPer * per; it += NW * kWave) {
-                const int q = it / per, c8 = it % per, c = p0 + c8 * 8;
-                if (h * kRowsPer + q >= nq || c >= a.N) continue;
-                const char *row = smem + q * BP * 4;
-                const int c4 = gated ? c8 / 2 * 8 + c8 % 2 * 2 : c8 * 2;
-                float v[8], up[8];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const f32x4 l = *reinterpret_cast<const f32x4 *>(row + ((c4 + k) ^ (q & 7)) * 16);
-                    f32x4 u = l;
-                    if (gated) u = *reinterpret_cast<const f32x4 *>(row + ((c4 + 4 + k) ^ (q & 7)) * 16);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[4 * k + i] = l[i], up[4 * k + i] = u[i];
-                }
-                finish(a, e, r0 + h * kRowsPer + q, c, v, up);
-            }
-        }
+        static_assert((BQ < 128 ? BQ : 128) * BP * 4 <= NST * kStage, "LDS");
+        if (gated) forward_rows<true, BQ, BP, NW>(a, smem, acc, e, r0, p0, nq, wq, wp, lane);
+        else forward_rows<false, BQ, BP, NW>(a, smem, acc, e, r0, p0, nq, wq, wp, lane);
     } else {
         static_assert(MODE == kForward || BQ * BP * 2 <= NST * kStage, "LDS");
         lds_barrier();
@@ -672,7 +696,7 @@ template <int MODE, bool FP8>
 hipError_t run(const ExpertArgs &a, hipStream_t st) {
     const int64_t each = MODE == kDw ? a.Nw : a.rows / a.E;
     if (each >= 256) return run_tile<MODE, FP8, 256, 256, 4, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
-    return run_tile<MODE, FP8, 128, 128, 2, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
+    return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
 }
 
 }  // namespace
