@@ -144,45 +144,60 @@ __device__ __forceinline__ bool locate(const ExpertArgs &a, int size, int cols, 
     return true;
 }
 
-__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
-    u32x4 o;
+// W neighbouring values, W 4 or 8.
+template <int W>
+__device__ __forceinline__ void store_bf16(uint16_t *to, const float (&v)[W]) {
+    typedef uint32_t bits __attribute__((ext_vector_type(W / 2)));
+    bits o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-    return o;
+    for (int i = 0; i < W / 2; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<bits *>(to) = o;
 }
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const f32x4 lo = reinterpret_cast<const f32x4 *>(p)[0], hi = reinterpret_cast<const f32x4 *>(p)[1];
+template <int W>
+__device__ __forceinline__ void load_bf16(const uint16_t *p, uint32_t (&v)[W / 2]) {
+    typedef uint32_t bits __attribute__((ext_vector_type(W / 2)));
+    const bits o = *reinterpret_cast<const bits *>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+    for (int i = 0; i < W / 2; ++i) v[i] = o[i];
+}
+template <int W>
+__device__ __forceinline__ void load_float(const float *p, float (&v)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+        const f32x4 o = *reinterpret_cast<const f32x4 *>(p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i + j] = o[j];
+    }
 }
 
-// Eight neighbouring outputs from the biased fp32 sums `v` (and, gated, those
-// of the up projection): the kept pre-activation, activation and residual.
-template <bool GATED>
-__device__ __forceinline__ void finish(const ExpertArgs &a, int64_t r, int c, float (&v)[8], const float (&up)[8], u32x4 res) {
+// W neighbouring outputs from the biased fp32 sums `v` (and, gated, those of
+// the up projection): the kept pre-activation, activation and residual.
+template <bool GATED, int W>
+__device__ __forceinline__ void finish(const ExpertArgs &a, int64_t r, int c, float (&v)[W], const float (&up)[W],
+                                       const uint32_t (&res)[W / 2]) {
     if (a.pre) {
         uint16_t *to = a.pre + r * a.Nw + c;
-        *reinterpret_cast<u32x4 *>(to) = pack8(v);
-        if (GATED) *reinterpret_cast<u32x4 *>(to + a.N) = pack8(up);
+        store_bf16<W>(to, v);
+        if (GATED) store_bf16<W>(to + a.N, up);
     }
     if (GATED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * logistic(v[i]) * up[i];
+        for (int i = 0; i < W; ++i) v[i] = v[i] * logistic(v[i]) * up[i];
     } else if (a.act == kActGelu) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate(kActGelu, v[i]);
+        for (int i = 0; i < W; ++i) v[i] = activate(kActGelu, v[i]);
     } else if (a.act == kActSilu) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate(kActSilu, v[i]);
+        for (int i = 0; i < W; ++i) v[i] = activate(kActSilu, v[i]);
     } else if (a.act == kActRelu) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate(kActRelu, v[i]);
+        for (int i = 0; i < W; ++i) v[i] = activate(kActRelu, v[i]);
     }
     if (a.residual) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += i % 2 ? bf16_hi(res[i / 2]) : bf16_lo(res[i / 2]);
+        for (int i = 0; i < W; ++i) v[i] += i % 2 ? bf16_hi(res[i / 2]) : bf16_lo(res[i / 2]);
     }
-    *reinterpret_cast<u32x4 *>(a.out + r * a.N + c) = pack8(v);
+    store_bf16<W>(a.out + r * a.N + c, v);
 }
 
 __device__ __forceinline__ void lds_barrier() {
@@ -200,24 +215,24 @@ template <bool GATED, int BQ, int BP, int NW, int NP, int NQ, typename ACC>
 __device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, ACC (&acc)[NP][NQ], int e, int64_t r0, int p0,
                                              int nq, int wq, int wp, int lane) {
     constexpr int kRowsPer = BQ < 128 ? BQ : 128, kPer = BP / (GATED ? 16 : 8);
-    constexpr int kApart = NW * kWave / kPer, kItems = kRowsPer / kApart;
+    constexpr int kApart = NW * kWave / kPer, kItems = (kRowsPer + kApart - 1) / kApart;
     const int c8 = threadIdx.x % kPer, q0 = threadIdx.x / kPer, c = p0 + c8 * 8;
     const int c4 = GATED ? c8 / 2 * 8 + c8 % 2 * 2 : c8 * 2;
     float bv[8], bu[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) bv[i] = bu[i] = 0.0f;
     if (a.bias && c < a.N) {
-        load8(a.bias + (int64_t)e * a.Nw + c, bv);
-        if (GATED) load8(a.bias + (int64_t)e * a.Nw + a.N + c, bu);
+        load_float<8>(a.bias + (int64_t)e * a.Nw + c, bv);
+        if (GATED) load_float<8>(a.bias + (int64_t)e * a.Nw + a.N + c, bu);
     }
 #pragma unroll
     for (int h = 0; h < BQ / kRowsPer; ++h) {
-        u32x4 res[kItems];
+        uint32_t res[kItems][4];
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int q = h * kRowsPer + q0 + k * kApart;
-            res[k] = u32x4{0u, 0u, 0u, 0u};
-            if (a.residual && q < nq && c < a.N) res[k] = *reinterpret_cast<const u32x4 *>(a.residual + (r0 + q) * a.N + c);
+            res[k][0] = res[k][1] = res[k][2] = res[k][3] = 0u;
+            if (a.residual && q0 + k * kApart < kRowsPer && q < nq && c < a.N) load_bf16<8>(a.residual + (r0 + q) * a.N + c, res[k]);
         }
         lds_barrier();
         if (wq / kRowsPer == h) {
@@ -234,7 +249,7 @@ __device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, AC
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
             const int q = q0 + k * kApart;
-            if (h * kRowsPer + q >= nq || c >= a.N) continue;
+            if (q >= kRowsPer || h * kRowsPer + q >= nq || c >= a.N) continue;
             const char *row = smem + q * BP * 4;
             float v[8], up[8];
 #pragma unroll
@@ -245,7 +260,7 @@ __device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, AC
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[4 * i + r] = l[r] + bv[4 * i + r], up[4 * i + r] = u[r] + bu[4 * i + r];
             }
-            finish<GATED>(a, r0 + h * kRowsPer + q, c, v, up, res[k]);
+            finish<GATED, 8>(a, r0 + h * kRowsPer + q, c, v, up, res[k]);
         }
     }
 }
@@ -411,11 +426,12 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
     auto next = [](int stage) { return stage + 1 == NST ? 0 : stage + 1; };
     // The oldest step's loads are done when those of NST - 2 steps may be out.
     constexpr int kLanded = (NST - 2) * kIssued;
-    static_assert(kLanded < kAnyLoads && (!FP8 || NST == 2), "the scales' loads are counted with the stage's");
+    // (Loads end in order, and a step's scales are issued before its operands.)
+    static_assert(kLanded < kAnyLoads, "vmcnt");
     if (steps > 0)
         for (int t = 0; t < NST - 1; ++t) issue(t, t);
     int rd = 0, wr = NST - 1;
-    if (NW == 8 && steps > 0) {
+    if constexpr (NW == 8) {
         // Two waves on each SIMD, of the two halves of the workgroup: one reads
         // its fragments while the other keeps the matrix unit, and at the next
         // barrier they change places; the second half runs one turn behind,
@@ -432,7 +448,7 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
         };
-        __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
+        if (steps > 0) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
         asm volatile("" ::: "memory");
         turn();
         if (second) turn();
@@ -696,6 +712,10 @@ template <int MODE, bool FP8>
 hipError_t run(const ExpertArgs &a, hipStream_t st) {
     const int64_t each = MODE == kDw ? a.Nw : a.rows / a.E;
     if (each >= 256) return run_tile<MODE, FP8, 256, 256, 4, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
+    if constexpr (MODE != kDw) {
+        if (each <= 32) return run_tile<MODE, FP8, 32, MODE == kForward ? 64 : 128, MODE == kForward ? 2 : 1, MODE == kForward ? 2 : 4, 128, MODE == kForward ? 6 : 4>(a, st);
+        if (each <= 64) return run_tile<MODE, FP8, 64, 128, 2, 2, 128, 3>(a, st);
+    }
     return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
 }
 
