@@ -580,12 +580,23 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
             }
         lds_barrier();
         uint16_t *to = MODE == kDx ? a.d_x + r0 * a.I : a.d_w + we + (int64_t)q0 * a.I;
-        for (int it = threadIdx.x; it < BQ * BP / 8; it += NW * kWave) {
-            const int q = it / (BP / 8), c = it % (BP / 8);
-            if (q < nq && p0 + c * 8 < P)
-                *reinterpret_cast<u32x4 *>(to + (int64_t)q * a.I + p0 + c * 8) =
-                    *reinterpret_cast<const u32x4 *>(smem + q * BP * 2 + (c ^ (q & 15)) * 16);
-        }
+        constexpr int kPer = BP / 8, kApart = NW * kWave / kPer, kItems = BQ / kApart, kOnce = kItems < 8 ? kItems : 8;
+        const int c = threadIdx.x % kPer, q0 = threadIdx.x / kPer;
+        to += (int64_t)q0 * a.I + p0 + c * 8;
+        if (p0 + c * 8 < P)
+#pragma unroll
+            for (int k0 = 0; k0 < kItems; k0 += kOnce) {
+                u32x4 v[kOnce];
+#pragma unroll
+                for (int k = 0; k < kOnce; ++k) {
+                    const int q = q0 + (k0 + k) * kApart;
+                    v[k] = *reinterpret_cast<const u32x4 *>(smem + q * BP * 2 + (c ^ (q & 15)) * 16);
+                }
+#pragma unroll
+                for (int k = 0; k < kOnce; ++k)
+                    if (q0 + (k0 + k) * kApart < nq)
+                        *reinterpret_cast<u32x4 *>(to + (int64_t)((k0 + k) * kApart) * a.I) = v[k];
+            }
     }
 }
 
@@ -708,15 +719,41 @@ hipError_t run_tile(const ExpertArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Microseconds that a product of `steps` 128-byte steps takes in tiles of BQ x
+// BP: so many rounds of as many tiles as the card holds at once, each with a
+// start and an epilogue; a step takes `full` in a round that fills the card,
+// `least` with one tile alone.  Measured on 16 experts of 4 to 1024 rows, 2048
+// to 2 x 1024 and 4096 to 2048 (at 192 rows: 72 us in 32-row tiles, 38 in
+// 64-row, 34 in 128-row, 46 in 256-row tiles; at 1024 rows 302, 160, 131, 116).
+double tile_cost(const ExpertArgs &a, bool dw, int columns, int BQ, int BP, int slots, int steps, double start,
+                 double least, double full) {
+    const int64_t some = a.rows < a.E ? a.rows : a.E;
+    int64_t tiles = a.rows / BQ + some / 2;  // on average half a tile is missing from each expert's last
+    tiles = dw ? (int64_t)a.E * ceil_div(a.Nw, BQ) : (tiles > some ? tiles : some);
+    tiles *= ceil_div(columns, BP);
+    const int64_t rounds = tiles / slots, rest = tiles % slots;
+    return rounds * (start + steps * full) + (rest ? start + steps * (least + (full - least) * rest / slots) : 0.0);
+}
+
 template <int MODE, bool FP8>
 hipError_t run(const ExpertArgs &a, hipStream_t st) {
-    const int64_t each = MODE == kDw ? a.Nw : a.rows / a.E;
-    if (each >= 256) return run_tile<MODE, FP8, 256, 256, 4, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
-    if constexpr (MODE != kDw) {
-        if (each <= 32) return run_tile<MODE, FP8, 32, MODE == kForward ? 64 : 128, MODE == kForward ? 2 : 1, MODE == kForward ? 2 : 4, 128, MODE == kForward ? 6 : 4>(a, st);
-        if (each <= 64) return run_tile<MODE, FP8, 64, 128, 2, 2, 128, 3>(a, st);
+    constexpr bool F = MODE == kForward, W = MODE == kDw;
+    const int K = F ? a.I : (W ? (int)(a.rows / a.E) : a.Nw), steps = ceil_div(K, FP8 ? 128 : 64);
+    const int columns = F ? a.Nw : a.I;
+    const double c256 = tile_cost(a, W, columns, 256, 256, 256, steps, 8, 1.1, 1.85);
+    const double c128 = tile_cost(a, W, columns, 128, 128, 512, steps, 5, 0.55, 1.15);
+    if constexpr (!W) {
+        const double c64 = tile_cost(a, W, columns, 64, 128, 512, steps, 3.5, 0.35, 0.7);
+        const double c32 = F ? tile_cost(a, W, columns, 32, 64, 512, steps, 3, 0.2, 0.32)
+                             : tile_cost(a, W, columns, 32, 128, 512, steps, 3, 0.3, 0.69);
+        const double best = c64 < c32 ? c64 : c32;
+        if (best <= c128 && best <= c256) {
+            if (c64 < c32) return run_tile<MODE, FP8, 64, 128, 2, 2, 128, 3>(a, st);
+            return run_tile<MODE, FP8, 32, F ? 64 : 128, F ? 2 : 1, F ? 2 : 4, 128, F ? 6 : 4>(a, st);
+        }
     }
-    return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
+    if (c128 < c256) return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
+    return run_tile<MODE, FP8, 256, 256, 4, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
 }
 
 }  // namespace
