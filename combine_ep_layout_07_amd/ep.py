@@ -159,8 +159,8 @@ def ep_query_sizes(cfg: EpConfig) -> EpSizes:
 # The helpers below run on every call, so they stay cheap: plain integers for
 # pointers and streams (the argtypes convert them), one size property.
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: a Stream object takes 2.5 us of a call's 8
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
