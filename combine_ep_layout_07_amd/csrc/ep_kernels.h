@@ -148,7 +148,9 @@ struct CombineBackwardArgs {
 
 // Blocks per source of the router's forward pass with the balance loss; each
 // leaves partial sums.
-int route_blocks(int S, int T, int E);
+int route_blocks(int S, int T, int E, int K);
+// Workgroups per source of its sum.
+int route_sum_blocks(int E);
 
 struct RouteArgs {
     int S, T, E, K;
@@ -166,6 +168,8 @@ struct RouteArgs {
     float *part_p;       // scratch [S*B][pitch]: sums of p; null without a balance loss
     int32_t *part_cnt;   // scratch [S*B][pitch]: chosen lanes
     int32_t *part_seen;  // scratch [S*B]: valid tokens
+    double *part_loss;   // scratch [S][route_sum_blocks]: shares of the loss
+    int32_t *part_done;  // scratch [S]: workgroups of the sum that have finished
     const float *d_weights, *d_loss;  // backward; either may be null
     void *d_logits;
 };

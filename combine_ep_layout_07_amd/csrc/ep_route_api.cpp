@@ -27,10 +27,16 @@ int check_config(const ep_route_config_t *c) {
 }
 
 uint64_t units(const ep_route_config_t *c) {
-    return (uint64_t)c->num_src_ranks * ep::route_blocks(c->num_src_ranks, c->num_tokens, c->num_experts);
+    return (uint64_t)c->num_src_ranks * ep::route_blocks(c->num_src_ranks, c->num_tokens, c->num_experts, c->num_topk);
 }
 
 int pitch(const ep_route_config_t *c) { return (c->num_experts + 3) / 4 * 4; }
+
+// Bytes of the scratch before the partial sums: shares of the loss, counters.
+uint64_t head_bytes(const ep_route_config_t *c) {
+    const uint64_t S = c->num_src_ranks;
+    return (S * ep::route_sum_blocks(c->num_experts) * 8 + S * 4 + 15) / 16 * 16;
+}
 
 // Shape and tables common to both directions.
 int make_args(const ep_route_config_t *c, const void *logits_dev, const uint8_t *token_mask_dev,
@@ -81,7 +87,7 @@ int ep_query_route_sizes(const ep_route_config_t *cfg, ep_route_sizes_t *sz) {
     sz->tokens_per_expert = S * E * sizeof(int32_t);
     sz->tokens_valid = S * sizeof(int32_t);
     sz->balance_loss = S * sizeof(float);
-    sz->scratch = units(cfg) * (2 * pitch(cfg) + 1) * 4;
+    sz->scratch = head_bytes(cfg) + units(cfg) * (2 * pitch(cfg) + 1) * 4;
     return EP_OK;
 }
 
@@ -96,7 +102,9 @@ int ep_route(const ep_route_config_t *cfg, const void *logits_dev, const float *
     a.bias = bias_dev;
     if (given) {
         const uint64_t words = units(cfg) * (uint64_t)a.pitch;
-        a.part_p = static_cast<float *>(route->scratch_dev);
+        a.part_loss = static_cast<double *>(route->scratch_dev);
+        a.part_done = reinterpret_cast<int32_t *>(a.part_loss + (uint64_t)a.S * ep::route_sum_blocks(a.E));
+        a.part_p = reinterpret_cast<float *>(static_cast<char *>(route->scratch_dev) + head_bytes(cfg));
         a.part_cnt = reinterpret_cast<int32_t *>(a.part_p + words);
         a.part_seen = a.part_cnt + words;
     }

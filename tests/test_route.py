@@ -357,3 +357,72 @@ def test_route_repeats_and_replays():
         assert all(torch.equal(a, b) for a, b in zip(values(), want))
         step()
         assert all(torch.equal(a, b) for a, b in zip(values(), want))
+
+
+# ------------------------------------------------------------------------------- many tokens: several tokens per wave
+
+MANY = [(1, 8193, 8, 2), (3, 2731, 31, 4), (1, 8192, 64, 6), (2, 4111, 100, 8), (1, 9000, 160, 11), (5, 1639, 192, 1),
+        (1, 8201, 256, 8), (1, 8192, 256, 15), (1, 8200, 260, 31), (2, 4100, 384, 6), (1, 8195, 512, 8), (1, 8192, 512, 32),
+        (1, 8192, 600, 8)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("S,T,E,K", MANY)
+def test_many_tokens(S, T, E, K, dtype, scoring):
+    rng = np.random.default_rng(S * 131 + T + E)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    mask = (rng.uniform(size=(S, T)) < 0.9).astype(np.uint8)
+    check(S, T, E, K, dtype, scoring, seed=3)
+    check(S, T, E, K, dtype, scoring, bias, mask, seed=4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_many_tokens_with_near_ties(scoring, biased):
+    """Keys that agree in their upper bits, in whole rows and at the border of the choice: whole keys decide."""
+    T, E, K = 8400, 256, 8
+    rng = np.random.default_rng(5)
+    x = 1.0 + rng.integers(0, 40, size=(1, T, E)).astype(np.float32) * np.float32(2.0 ** -23)
+    x[0, ::3] = rng.integers(0, 6, size=(2800, E)) * 0.25  # equal values: the lowest index
+    bias = (rng.integers(-3, 4, size=E) * 2.0 ** -22).astype(np.float32) if biased else None
+    check(1, T, E, K, "fp32", scoring, bias, logits=torch.from_numpy(x), seed=9)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_many_tokens_masked_and_special(dtype, scoring):
+    S, T, E, K = 2, 4200, 130, 6
+    x, rng = make(S, T, E, dtype, 13)
+    x[0, 0:4200:7] = float("-inf")
+    x[0, 1:4200:7] = low_of(dtype)
+    x[0, 2:4200:7] = float("nan")
+    x[0, 3:4200:7, 4:] = float("-inf")
+    x[0, 4:4200:7, ::2] = float("nan")
+    x[1, 5:4200:7, 7] = float("inf")
+    x[1, 6:4200:7] *= 4.0
+    bias = np.linspace(-0.1, 0.1, E).astype(np.float32)
+    mask = (rng.uniform(size=(S, T)) < 0.5).astype(np.uint8)
+    for b, m in ((None, None), (bias, None), (bias, mask)):
+        f, got = check(S, T, E, K, dtype, scoring, b, m, logits=x, seed=14)
+        assert np.isfinite(got).all()
+
+
+@pytest.mark.gpu
+def test_many_tokens_on_unaligned_rows():
+    for dtype in (torch.float32, torch.bfloat16):
+        cfg = ep.make_route_config(1, 8200, 64, 4, "bf16" if dtype == torch.bfloat16 else "fp32")
+        flat = torch.randn(8200 * 64 + 1, device="cuda").to(dtype)
+        a, b = ep.alloc_route(cfg, balance=True), ep.alloc_route(cfg, balance=True)
+        dw, dl = torch.randn((1, 8200, 4), device="cuda"), torch.ones(1, device="cuda")
+        ep.ep_route(cfg, flat[1:], a)
+        ep.ep_route(cfg, flat[1:].clone(), b)
+        assert torch.equal(a.topk_idx, b.topk_idx) and torch.equal(a.topk_weights, b.topk_weights)
+        assert torch.equal(a.balance_loss, b.balance_loss)
+        ga, gb = torch.zeros_like(flat), torch.zeros_like(flat)
+        ep.ep_route_backward(cfg, flat[1:], a, dw, dl, ga[1:])
+        ep.ep_route_backward(cfg, flat[1:].clone(), b, dw, dl, gb)
+        assert torch.equal(ga[1:], gb[:-1])
