@@ -63,10 +63,21 @@ struct Loader {
     uint32_t bytes;  // rows at or past the tile's end lie outside
     int place;       // ALONG: the lane's chunk; else its k row in the wave's first load
 
-    __device__ __forceinline__ static int row(int j, int wave, int lane) { return (j * NW + wave) * kRows + lane / kLanes; }
-    __device__ __forceinline__ static int chunk(int r, int lane) {
-        if (!ALONG) return (lane % kLanes) ^ (((r & 3) | (r & 8) >> 1) << 1);
-        return (lane % kLanes) ^ (SB == 128 ? r & 7 : r / 2 & 3);
+    // `rows` rows (ALONG) or columns from `from` on, `pitch` bytes apart; gated:
+    // alternating 16 of the gate, 16 of the up projection, whose rows are apart.
+    // Along k the offsets grow with the row, so a bound at the end of the last
+    // row turns the rows after it into zeros.  Across k columns outside do so by
+    // the lane's offset, rows of k by issue's `left`.
+    __device__ __forceinline__ void init(const char *from, uint32_t pitch, int rows, bool gated, int wave, int lane) {
+        const int r = wave * kRows + lane / kLanes;
+        int c = (lane % kLanes) ^ (((r & 3) | (r & 8) >> 1) << 1);
+        if (ALONG) c = (lane % kLanes) ^ (SB == 128 ? r & 7 : r / 2 & 3);
+        at = from;
+        step = ALONG ? SB : SB / 2 * (int64_t)pitch;
+        off = ALONG || c * 8 < rows ? (gated ? r / 32 * 16 + r % 16 : r) * pitch + c * 16 : kOutside;
+        apart = NW * kRows / (gated ? 2 : 1) * pitch;
+        bytes = !ALONG ? kOutside : (rows > 0 ? (rows - 1) * pitch + SB : 0);
+        place = ALONG ? c : r;
     }
     // Issues the loads of one stage; `left` chunks (ALONG) or rows of k remain
     // (none: zeros, so that every step has as many loads).
@@ -207,11 +218,18 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// First column in the tile of a wave's fragment i; the wide tile's waves take
+// columns of both halves.
+template <int NP, bool WIDE>
+__device__ __forceinline__ int column_of(int wp, int i) {
+    return WIDE ? i / (NP / 2) * 128 + wp + i % (NP / 2) * 16 : wp + i * 16;
+}
+
 // The forward tile through LDS in fp32, as many rows at a time as fit, and the
 // epilogue in row order: a thread keeps its eight columns, so their bias is
 // loaded once, and has the residual of all its rows in flight before the sums
 // are in LDS (loaded row by row the epilogue took half of a small product).
-template <bool GATED, int BQ, int BP, int NW, int NP, int NQ, typename ACC>
+template <bool GATED, int BQ, int BP, int NW, int NP, int NQ, bool WIDE, typename ACC>
 __device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, ACC (&acc)[NP][NQ], int e, int64_t r0, int p0,
                                              int nq, int wq, int wp, int lane) {
     constexpr int kRowsPer = BQ < 128 ? BQ : 128, kPer = BP / (GATED ? 16 : 8);
@@ -240,7 +258,7 @@ __device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, AC
             for (int i = 0; i < NP; ++i)
 #pragma unroll
                 for (int j = 0; j < NQ; ++j) {
-                    const int q = wq % kRowsPer + j * 16 + lane % 16, at = (wp + i * 16) / 4 + lane / 16;
+                    const int q = wq % kRowsPer + j * 16 + lane % 16, at = column_of<NP, WIDE>(wp, i) / 4 + lane / 16;
                     *reinterpret_cast<f32x4 *>(smem + q * BP * 4 + (at ^ (q & 7)) * 16) =
                         f32x4{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
                 }
@@ -280,74 +298,161 @@ struct Sum<true> {
     typedef Four type;
 };
 
+// A tile's place: rows r0 .. r0 + nq of Q's side, columns p0 .. of P's, and the
+// bases of both operands at k = 0.
+struct Tile {
+    int64_t r0, we;  // first row, first weight of the expert
+    const char *q, *p;
+    uint32_t pitchq, pitchp;  // bytes between rows
+    int e, K, nq, np, q0, p0;
+};
+
+template <int MODE, bool FP8, int BQ, int BP>
+__device__ __forceinline__ bool find(const ExpertArgs &a, int cols, Tile &t) {
+    constexpr int EL = FP8 ? 1 : 2;
+    int tcol;
+    Segment g;
+    t.q0 = 0;
+    if (MODE == kDw) {
+        const int per = (a.Nw + BQ - 1) / BQ;
+        int trow;
+        if (!place_tile(blockIdx.x, per * a.E, cols, trow, tcol)) return false;
+        g = segment_of(a.base, trow / per, a.rows);
+        t.q0 = trow % per * BQ;
+    } else if (!locate(a, BQ, cols, g, tcol)) {
+        return false;
+    }
+    const bool gated = MODE == kForward && a.act == kActSwiglu;
+    t.r0 = uniform64(g.r0);
+    t.e = uniform(g.e);
+    const int n = uniform(g.n);
+    t.we = (int64_t)t.e * a.Nw * a.I;
+    t.K = MODE == kForward ? a.I : (MODE == kDx ? a.Nw : n);
+    t.p0 = tcol * (gated ? BP / 2 : BP);
+    t.np = min((MODE == kForward ? a.N : a.I) - t.p0, gated ? BP / 2 : BP);
+    t.nq = MODE == kDw ? min(a.Nw - t.q0, BQ) : n;
+    const char *d = reinterpret_cast<const char *>(a.d), *x = static_cast<const char *>(a.x), *w = static_cast<const char *>(a.w);
+    const uint32_t pitchx = a.I * EL, pitchd = a.Nw * 2;
+    t.pitchq = MODE == kForward ? pitchx : pitchd;
+    t.pitchp = pitchx;
+    if (MODE == kForward) t.q = x + t.r0 * pitchx, t.p = w + (t.we + (int64_t)t.p0 * a.I) * EL;
+    else if (MODE == kDx) t.q = d + t.r0 * pitchd, t.p = w + (t.we + t.p0) * 2;
+    else t.q = d + t.r0 * pitchd + (int64_t)t.q0 * 2, t.p = x + t.r0 * pitchx + (int64_t)t.p0 * 2;
+    return true;
+}
+
+// The fp8 scales of eight steps at a time in LDS, [row][8] for x, and for the
+// weights the tile's two or three blocks of 128 weight rows: its columns', or
+// gated the gate's one and the up projection's two at most.  (Loaded by each
+// lane at each step they took a third of the time: a line for every row, every
+// time anew.)
+constexpr int kBlocks = 8;
+template <int BQ, int NW>
+__device__ __forceinline__ void load_scales(const ExpertArgs &a, const Tile &t, float (*sxs)[BQ * kBlocks], float (*sws)[kWave],
+                                            bool gated, int kb0, int wave, int lane) {
+    const int to = kb0 / kBlocks % 2, kb = kb0 + lane % kBlocks, nkb = a.I / 128;
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(a.x_sf + t.r0 * nkb), 0, kOutside, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < BQ * kBlocks / kWave / NW; ++j) {
+        const int row = (j * NW + wave) * (kWave / kBlocks) + lane / kBlocks;
+        const uint32_t o = row < t.nq && kb < nkb ? (row * nkb + kb) * 4 : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char *)&sxs[to][(j * NW + wave) * kWave], 4, o, 0, 0, 0);
+    }
+    if (wave == 0) {
+        const int blocks = (a.Nw + 127) / 128, slot = lane / kBlocks;
+        const int block = gated && slot > 0 ? (a.N + t.p0) / 128 + slot - 1 : t.p0 / 128 + slot;
+        const uint32_t o = slot < 3 && block < blocks && kb < nkb ? (block * nkb + kb) * 4 : kOutside;
+        const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<float *>(a.w_sf + (int64_t)t.e * blocks * nkb), 0, kOutside, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_char *)&sws[to][0], 4, o, 0, 0, 0);
+    }
+}
+// The step's scale of a row of x, and of the weights' columns: [0] the first
+// block (gated: the gate's), [1] the second (the up projection's first), [2]
+// the up projection's second.
+__device__ __forceinline__ float x_scale(const float *sxs, int row, int step) { return sxs[row * kBlocks + step % kBlocks]; }
+__device__ __forceinline__ f32x4 w_scales(const float *sws, int step) {
+    const float *s = sws + step % kBlocks;
+    return f32x4{s[0], s[kBlocks], s[2 * kBlocks], 0.0f};
+}
+
+__device__ __forceinline__ i32x8 join(bf16x8 lo, bf16x8 hi) {
+    return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ f32x4 mfma8(i32x8 p, i32x8 q) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ void add_scaled(Four &c, f32x4 part, float sc) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c[r] = fmaf(part[r], sc, c[r]);
+    // Here and not later: left to itself the compiler holds the products of a
+    // whole step until its end, which spills.
+    asm volatile("" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
+}
+
+// The finished tile leaves through LDS, so that rows go out in 16-byte pieces
+// of whole lines (stored from the accumulators they go as 8-byte pieces of 16
+// rows: 12 us per 256 x 256 tile), gradients already rounded.
+template <int MODE, int BQ, int BP, int NW, int NP, int NQ, bool WIDE, typename ACC>
+__device__ __forceinline__ void put_tile(const ExpertArgs &a, char *smem, ACC (&acc)[NP][NQ], const Tile &t, int wq, int wp, int lane) {
+    __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
+    if (MODE == kForward) {
+        if (a.act == kActSwiglu) forward_rows<true, BQ, BP, NW, NP, NQ, WIDE>(a, smem, acc, t.e, t.r0, t.p0, t.nq, wq, wp, lane);
+        else forward_rows<false, BQ, BP, NW, NP, NQ, WIDE>(a, smem, acc, t.e, t.r0, t.p0, t.nq, wq, wp, lane);
+        return;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+            const int q = wq + j * 16 + lane % 16, p = column_of<NP, WIDE>(wp, i) + lane / 16 * 4;
+            *reinterpret_cast<u32x2 *>(smem + q * BP * 2 + (p / 8 ^ (q & 15)) * 16 + p % 8 * 2) =
+                u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
+        }
+    lds_barrier();
+    constexpr int kPer = BP / 8, kApart = NW * kWave / kPer, kItems = BQ / kApart, kOnce = kItems < 8 ? kItems : 8;
+    const int c = threadIdx.x % kPer, q0 = threadIdx.x / kPer;
+    if (c * 8 >= t.np) return;
+    uint16_t *to = (MODE == kDx ? a.d_x + t.r0 * a.I : a.d_w + t.we + (int64_t)t.q0 * a.I) + (int64_t)q0 * a.I + t.p0 + c * 8;
+#pragma unroll
+    for (int k0 = 0; k0 < kItems; k0 += kOnce) {
+        u32x4 v[kOnce];
+#pragma unroll
+        for (int k = 0; k < kOnce; ++k) {
+            const int q = q0 + (k0 + k) * kApart;
+            v[k] = *reinterpret_cast<const u32x4 *>(smem + q * BP * 2 + (c ^ (q & 15)) * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < kOnce; ++k)
+            if (q0 + (k0 + k) * kApart < t.nq) *reinterpret_cast<u32x4 *>(to + (int64_t)((k0 + k) * kApart) * a.I) = v[k];
+    }
+}
+
+// Tiles of up to 128 x 128 by four waves, two workgroups on a CU: one reads
+// while the other multiplies, by chance.  SB bytes of k per step, NST stages.
 template <int MODE, bool FP8, int BQ, int BP, int WQ, int WP, int SB, int NST>
 __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, int cols) {
     constexpr int NW = WQ * WP, NQ = BQ / WQ / 16, NP = BP / WP / 16;
     constexpr bool QA = MODE != kDw, PA = MODE == kForward;
     constexpr int kStage = (BQ + BP) * SB;
     __shared__ __align__(1024) char smem[NST * kStage];
+    __shared__ float sxs[2][FP8 ? BQ * kBlocks : 1], sws[2][FP8 ? kWave : 1];
     const int lane = lane_id(), wave = uniform(threadIdx.x / kWave);
     const int wq = wave % WQ * (BQ / WQ), wp = wave / WQ * (BP / WP);
     const bool gated = MODE == kForward && a.act == kActSwiglu;
-    int tcol, q0 = 0;
-    Segment g;
-    if (MODE == kDw) {
-        const int per = (a.Nw + BQ - 1) / BQ;
-        int trow;
-        if (!place_tile(blockIdx.x, per * a.E, cols, trow, tcol)) return;
-        g = segment_of(a.base, trow / per, a.rows);
-        q0 = trow % per * BQ;
-    } else if (!locate(a, BQ, cols, g, tcol)) {
-        return;
-    }
-    const int64_t r0 = uniform64(g.r0);
-    const int e = uniform(g.e), n = uniform(g.n);
-    constexpr int EL = FP8 ? 1 : 2;
-    const int K = MODE == kForward ? a.I : (MODE == kDx ? a.Nw : n);
-    const int64_t pitchx = (int64_t)a.I * EL, pitchd = (int64_t)a.Nw * 2;
-    const int64_t we = (int64_t)e * a.Nw * a.I;
-    const int P = MODE == kForward ? a.N : a.I;  // output columns
-    const int p0 = tcol * (gated ? BP / 2 : BP);
-    const int nq = MODE == kDw ? min(a.Nw - q0, BQ) : n;
+    Tile t;
+    if (!find<MODE, FP8, BQ, BP>(a, cols, t)) return;
 
     Loader<QA, BQ, NW, SB> lq;
     Loader<PA, BP, NW, SB> lp;
-    const char *d = reinterpret_cast<const char *>(a.d), *x = static_cast<const char *>(a.x), *w = static_cast<const char *>(a.w);
-    if (MODE == kForward) {
-        lq.at = x + r0 * pitchx;
-        lp.at = w + (we + (int64_t)p0 * a.I) * EL;
-        // Rows of the tile alternate between 16 of the gate and 16 of the up
-        // projection; all of a wave's loads lie in one of the two.
-        static_assert(MODE != kForward || NW * lp.kRows % 32 == 0, "a wave's loads keep their side");
-        if (gated && wave * lp.kRows / 16 % 2) lp.at += (int64_t)a.N * pitchx;
-    } else if (MODE == kDx) {
-        lq.at = d + r0 * pitchd;
-        lp.at = w + (we + p0) * 2;
-    } else {
-        lq.at = d + r0 * pitchd + (int64_t)q0 * 2;
-        lp.at = x + r0 * pitchx + (int64_t)p0 * 2;
-    }
-    lq.step = QA ? SB : SB / 2 * pitchd;
-    lp.step = PA ? SB : SB / 2 * pitchx;
-    {
-        // Along k: the offsets grow with the row, so a bound at the end of the
-        // tile's last row turns the rows after it into zeros.  Across k: columns
-        // outside by the lane's offset, rows of k by `left`.
-        const int r = lq.row(0, wave, lane), c = lq.chunk(r, lane);
-        const uint32_t pitch = (uint32_t)(QA && MODE == kForward ? pitchx : pitchd);
-        lq.off = QA || c * 8 < nq ? r * pitch + c * 16 : kOutside;
-        lq.apart = NW * lq.kRows * pitch;
-        lq.bytes = QA ? (nq - 1) * pitch + SB : kOutside;
-        lq.place = QA ? c : r;
-    }
-    {
-        const int r = lp.row(0, wave, lane), c = lp.chunk(r, lane);
-        const uint32_t pitch = (uint32_t)pitchx;
-        lp.off = PA || p0 + c * 8 < P ? (gated ? r / 32 * 16 + r % 16 : r) * pitch + c * 16 : kOutside;
-        lp.apart = NW * lp.kRows / (gated ? 2 : 1) * pitch;
-        lp.bytes = PA ? (min(P - p0, gated ? BP / 2 : BP) - 1) * pitch + SB : kOutside;
-        lp.place = PA ? c : r;
-    }
+    lq.init(t.q, t.pitchq, t.nq, false, wave, lane);
+    lp.init(t.p, t.pitchp, t.np, gated, wave, lane);
+    // Rows of the tile alternate between 16 of the gate and 16 of the up
+    // projection; all of a wave's loads lie in one of the two.
+    static_assert(MODE != kForward || NW * lp.kRows % 32 == 0, "a wave's loads keep their side");
+    if (gated && wave * lp.kRows / 16 % 2) lp.at += (int64_t)a.N * t.pitchp;
     Reader<QA, BQ, SB> rq;
     Reader<PA, BP, SB> rp;
     rq.init(wq, lane);
@@ -361,243 +466,237 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
 
-    // fp8: the scales of eight steps at a time go to LDS, [row][8] for x, and
-    // for the weights the tile's two or three blocks of 128 weight rows: its
-    // columns', or gated the gate's one and the up projection's two at most.
-    // (Loaded by each lane at each step they took a third of the time: a line
-    // for every row, every time anew.)
-    constexpr int kBlocks = 8;
-    __shared__ float sxs[FP8 ? 2 : 1][FP8 ? BQ * kBlocks : 1], sws[FP8 ? 2 : 1][FP8 ? kWave : 1];
-    const int nkb = a.I / 128;
-    const int up_from = ((a.N + p0) / 128 + 1) * 128 - a.N - p0 - wp / 2;  // the wave's columns from here on take the third
-    auto load_scales = [&](int kb0) {
-        const int to = kb0 / kBlocks % 2, kb = kb0 + lane % kBlocks;
-        const __amdgpu_buffer_rsrc_t rx =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(a.x_sf + r0 * nkb), 0, kOutside, 0x00020000);
-#pragma unroll
-        for (int j = 0; j < BQ * kBlocks / kWave / NW; ++j) {
-            const int row = (j * NW + wave) * (kWave / kBlocks) + lane / kBlocks;
-            const uint32_t o = row < nq && kb < nkb ? (row * nkb + kb) * 4 : kOutside;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char *)&sxs[to][(j * NW + wave) * kWave], 4, o, 0, 0, 0);
-        }
-        if (wave == 0) {
-            const int blocks = (a.Nw + 127) / 128, slot = lane / kBlocks;
-            const int block = gated && slot > 0 ? (a.N + p0) / 128 + slot - 1 : p0 / 128 + slot;
-            const uint32_t o = slot < 3 && block < blocks && kb < nkb ? (block * nkb + kb) * 4 : kOutside;
-            const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-                const_cast<float *>(a.w_sf + (int64_t)e * blocks * nkb), 0, kOutside, 0x00020000);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_char *)&sws[to][0], 4, o, 0, 0, 0);
-        }
-    };
-    auto x_scale = [&](int t, int j) {
-        return sxs[t / kBlocks % 2][(wq + j * 16 + lane % 16) * kBlocks + t % kBlocks];
-    };
-    // The scales of even and of odd 16 columns of the wave, the latter up to
-    // and from up_from on.
-    auto w_scales = [&](int t) {
-        const float *s = &sws[t / kBlocks % 2][t % kBlocks];
-        const float first = s[gated ? 0 : wp / 128 * kBlocks], lo = s[kBlocks], hi = s[2 * kBlocks];
-        return f32x4{first, gated ? lo : first, gated ? hi : first, 0.0f};
-    };
-    auto w_scale = [&](f32x4 s, int i) { return i % 2 == 0 ? s[0] : (i / 2 * 16 + lane / 16 * 4 < up_from ? s[1] : s[2]); };
-    auto both = [](bf16x8 lo, bf16x8 hi) {
-        return __builtin_shufflevector(__builtin_bit_cast(i32x4, lo), __builtin_bit_cast(i32x4, hi), 0, 1, 2, 3, 4, 5, 6, 7);
-    };
-    auto mfma8 = [](i32x8 p, i32x8 q) {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-    };
-    auto add_scaled = [](typename Sum<FP8>::type &c, f32x4 part, float sc) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) c[r] = fmaf(part[r], sc, c[r]);
-        // Here and not later: left to itself the compiler holds the products of
-        // a whole step until its end, which spills.
-        asm volatile("" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
-    };
-
-    constexpr int kPerStep = SB / EL, kIssued = lq.kLoads + lp.kLoads;
-    const int steps = (K + kPerStep - 1) / kPerStep;
-    auto issue = [&](int t, int stage) {
-        if (FP8 && t % kBlocks == 0 && t < steps) load_scales(t);
-        const int left = K - t * kPerStep;
+    constexpr int EL = FP8 ? 1 : 2, kPerStep = SB / EL, kIssued = lq.kLoads + lp.kLoads;
+    const int steps = (t.K + kPerStep - 1) / kPerStep;
+    auto issue = [&](int s, int stage) {
+        if constexpr (FP8)
+            if (s % kBlocks == 0 && s < steps) load_scales<BQ, NW>(a, t, sxs, sws, gated, s, wave, lane);
+        const int left = t.K - s * kPerStep;
         char *to = smem + stage * kStage;
         lq.issue(to, wave, QA ? left / (16 / EL) : left);
         lp.issue(to + BQ * SB, wave, PA ? left / (16 / EL) : left);
     };
     auto next = [](int stage) { return stage + 1 == NST ? 0 : stage + 1; };
     // The oldest step's loads are done when those of NST - 2 steps may be out.
-    constexpr int kLanded = (NST - 2) * kIssued;
     // (Loads end in order, and a step's scales are issued before its operands.)
+    constexpr int kLanded = (NST - 2) * kIssued;
     static_assert(kLanded < kAnyLoads, "vmcnt");
     if (steps > 0)
-        for (int t = 0; t < NST - 1; ++t) issue(t, t);
+        for (int s = 0; s < NST - 1; ++s) issue(s, s);
     int rd = 0, wr = NST - 1;
-    if constexpr (NW == 8) {
-        // Two waves on each SIMD, of the two halves of the workgroup: one reads
-        // its fragments while the other keeps the matrix unit, and at the next
-        // barrier they change places; the second half runs one turn behind,
-        // held by one barrier more at the start.  fp8 has two such turns per
-        // step (the halves of P; all fragments of a step would not fit the
-        // registers).  A stage is written again from the turn after the second
-        // half's last read of it on.  Each wave waits for its own loads in the
-        // last turn before the first half reads them.
-        constexpr int kTurns = FP8 ? 2 : 1;
-        static_assert(NW != 8 || (FP8 ? SB == 128 : SB == 64), "one turn's fragments");
-        const bool second = wave >= 4;
-        auto turn = [] {
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        if (steps > 0) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
+    const int up_from = ((a.N + t.p0) / 128 + 1) * 128 - a.N - t.p0;  // gated: up columns from here on take the third scale
+    for (int s = 0; s < steps; ++s) {
+        // The step's loads have landed, and every wave is done with the stage
+        // that is written next.
+        __builtin_amdgcn_s_waitcnt(wait_for(kLanded, 0));
         asm volatile("" ::: "memory");
-        turn();
-        if (second) turn();
-        for (int t = 0; t < steps; ++t) {
-            const char *sq = smem + rd * kStage, *sp = sq + BQ * SB;
-            i32x8 wideq[FP8 ? NQ : 1], widep[FP8 ? NP / 2 : 1];
-            float xs[FP8 ? NQ : 1];
-            f32x4 ws;
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        issue(s + NST - 1, wr);
+        const char *sq = smem + rd * kStage, *sp = sq + BQ * SB;
+        if constexpr (!FP8) {
 #pragma unroll
-            for (int h = 0; h < kTurns; ++h) {
-                const int p1 = h * (NP / 2);
-                asm volatile("" ::: "memory");
-                bf16x8 fq[FP8 ? 1 : NQ], fp[FP8 ? 1 : NP];
-                if (FP8) {
-                    if (h == 0) {
-                        ws = w_scales(t);
+            for (int kk = 0; kk < SB / 64; ++kk) {
+                bf16x8 fq[NQ], fp[NP];
 #pragma unroll
-                        for (int j = 0; j < NQ; ++j) {
-                            xs[j] = x_scale(t, j);
-                            wideq[j] = both(rq.read(sq, j, 0), rq.read(sq, j, 1));
-                        }
-                    }
+                for (int j = 0; j < NQ; ++j) fq[j] = rq.read(sq, j, kk);
 #pragma unroll
-                    for (int i = 0; i < NP / 2; ++i) widep[i] = both(rp.read(sp, p1 + i, 0), rp.read(sp, p1 + i, 1));
-                } else {
+                for (int i = 0; i < NP; ++i) fp[i] = rp.read(sp, i, kk);
 #pragma unroll
-                    for (int j = 0; j < NQ; ++j) fq[j] = rq.read(sq, j, 0);
+                for (int i = 0; i < NP; ++i)
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) fp[i] = rp.read(sp, i, 0);
-                }
-                if (h == 0) issue(t + NST - 1, wr);
-                asm volatile("" ::: "memory");
-                if (h == kTurns - 1 && second) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, 0));
-                else __builtin_amdgcn_s_waitcnt(wait_for(kAnyLoads, 0));
-                turn();
-                __builtin_amdgcn_s_setprio(1);
-                if constexpr (FP8) {
-                    // Two products, and the scaling of the two before, at a time.
-                    constexpr int kPairs = NP / 2 * NQ / 2;
-                    f32x4 part[2][2];
-#pragma unroll
-                    for (int u = 0; u <= kPairs; ++u) {
-#pragma unroll
-                        for (int v = 0; v < 2 && u < kPairs; ++v)
-                            part[u % 2][v] = mfma8(widep[u * 2 / NQ], wideq[u * 2 % NQ + v]);
-#pragma unroll
-                        for (int v = 0; v < 2 && u > 0; ++v) {
-                            const int i = p1 + (u - 1) * 2 / NQ, j = (u - 1) * 2 % NQ + v;
-                            add_scaled(acc[i][j], part[(u - 1) % 2][v], xs[j] * w_scale(ws, i));
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i)
-#pragma unroll
-                        for (int j = 0; j < NQ; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
-                }
-                __builtin_amdgcn_s_setprio(0);
-                asm volatile("" ::: "memory");
-                if (h == kTurns - 1 && !second) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
-                turn();
+                    for (int j = 0; j < NQ; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
             }
-            rd = next(rd);
-            wr = next(wr);
-        }
-        if (!second) turn();
-    } else {
-        for (int t = 0; t < steps; ++t) {
-            // The step's loads have landed, and every wave is done with the
-            // stage that is written next.
-            __builtin_amdgcn_s_waitcnt(wait_for(kLanded, 0));
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            issue(t + NST - 1, wr);
-            const char *sq = smem + rd * kStage, *sp = sq + BQ * SB;
-            if constexpr (!FP8) {
-#pragma unroll
-                for (int kk = 0; kk < SB / 64; ++kk) {
-                    bf16x8 fq[NQ], fp[NP];
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) fq[j] = rq.read(sq, j, kk);
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) fp[i] = rp.read(sp, i, kk);
-#pragma unroll
-                    for (int i = 0; i < NP; ++i)
-#pragma unroll
-                        for (int j = 0; j < NQ; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp[i], fq[j], acc[i][j], 0, 0, 0);
-                }
-            } else {
-                i32x8 fq[NQ];
-                float xs[NQ];
-                const f32x4 ws = w_scales(t);
-#pragma unroll
-                for (int j = 0; j < NQ; ++j) xs[j] = x_scale(t, j), fq[j] = both(rq.read(sq, j, 0), rq.read(sq, j, 1));
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const i32x8 fp = both(rp.read(sp, i, 0), rp.read(sp, i, 1));
-#pragma unroll
-                    for (int j = 0; j < NQ; ++j) add_scaled(acc[i][j], mfma8(fp, fq[j]), xs[j] * w_scale(ws, i));
-                }
-            }
-            rd = next(rd);
-            wr = next(wr);
-        }
-    }
-
-    // The tile goes through LDS, so that rows leave in 16-byte pieces of whole
-    // lines (stored from the accumulators they leave as 8-byte pieces of 16
-    // rows: 12 us per 256 x 256 tile), gradients already rounded.
-    __builtin_amdgcn_s_waitcnt(wait_for(0, 0));
-    if (MODE == kForward) {
-        static_assert((BQ < 128 ? BQ : 128) * BP * 4 <= NST * kStage, "LDS");
-        if (gated) forward_rows<true, BQ, BP, NW>(a, smem, acc, e, r0, p0, nq, wq, wp, lane);
-        else forward_rows<false, BQ, BP, NW>(a, smem, acc, e, r0, p0, nq, wq, wp, lane);
-    } else {
-        static_assert(MODE == kForward || BQ * BP * 2 <= NST * kStage, "LDS");
-        lds_barrier();
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
+        } else {
+            i32x8 fq[NQ];
+            float xs[NQ];
+            const float *sx = sxs[s / kBlocks % 2];
+            const f32x4 ws = w_scales(sws[s / kBlocks % 2], s);
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
-                const int q = wq + j * 16 + lane % 16, p = wp + i * 16 + lane / 16 * 4;
-                *reinterpret_cast<u32x2 *>(smem + q * BP * 2 + (p / 8 ^ (q & 15)) * 16 + p % 8 * 2) =
-                    u32x2{pack_bf16(acc[i][j][0], acc[i][j][1]), pack_bf16(acc[i][j][2], acc[i][j][3])};
+                xs[j] = x_scale(sx, wq + j * 16 + lane % 16, s);
+                fq[j] = join(rq.read(sq, j, 0), rq.read(sq, j, 1));
             }
-        lds_barrier();
-        uint16_t *to = MODE == kDx ? a.d_x + r0 * a.I : a.d_w + we + (int64_t)q0 * a.I;
-        constexpr int kPer = BP / 8, kApart = NW * kWave / kPer, kItems = BQ / kApart, kOnce = kItems < 8 ? kItems : 8;
-        const int c = threadIdx.x % kPer, q0 = threadIdx.x / kPer;
-        to += (int64_t)q0 * a.I + p0 + c * 8;
-        if (p0 + c * 8 < P)
 #pragma unroll
-            for (int k0 = 0; k0 < kItems; k0 += kOnce) {
-                u32x4 v[kOnce];
+            for (int i = 0; i < NP; ++i) {
+                const i32x8 fp = join(rp.read(sp, i, 0), rp.read(sp, i, 1));
+                const float up = wp / 2 + i / 2 * 16 + lane / 16 * 4 < up_from ? ws[1] : ws[2];
+                const float wsc = gated && i % 2 ? up : ws[0];
 #pragma unroll
-                for (int k = 0; k < kOnce; ++k) {
-                    const int q = q0 + (k0 + k) * kApart;
-                    v[k] = *reinterpret_cast<const u32x4 *>(smem + q * BP * 2 + (c ^ (q & 15)) * 16);
-                }
-#pragma unroll
-                for (int k = 0; k < kOnce; ++k)
-                    if (q0 + (k0 + k) * kApart < nq)
-                        *reinterpret_cast<u32x4 *>(to + (int64_t)((k0 + k) * kApart) * a.I) = v[k];
+                for (int j = 0; j < NQ; ++j) add_scaled(acc[i][j], mfma8(fp, fq[j]), xs[j] * wsc);
             }
+        }
+        rd = next(rd);
+        wr = next(wr);
     }
+    static_assert((MODE == kForward ? (BQ < 128 ? BQ : 128) * BP * 4 : BQ * BP * 2) <= NST * kStage, "LDS");
+    put_tile<MODE, BQ, BP, NW, NP, NQ, false>(a, smem, acc, t, wq, wp, lane);
+}
+
+// Tiles of 256 x 256 by eight waves, one workgroup on a CU.
+//
+// Two waves on each SIMD, of the two halves of the workgroup: one reads its
+// fragments while the other keeps the matrix unit, and at the next barrier they
+// change places; the second half runs one turn behind, held by one barrier more
+// at the start.  A step is 128 bytes of k (whole lines: half lines cost the L2
+// twice the requests) in two turns: Q's fragments and those of P's first half,
+// then those of P's second half.
+//
+// LDS is a ring of R units of 16 KiB: the halves of 128 rows of Q (0, 1) and of
+// P (2, 3) of a step.  Units 0 to 2 are free when the second half has read them
+// in its first turn, unit 3 after its second, and each is refilled from the
+// next turn on with the unit R further: one in a step's first turn, three in
+// its second, two loads per wave each.  So R - 4 units are on their way at
+// every wait, 6 to 10 turns before they are read.  (In stages of whole steps,
+// or of half lines, the same product took 15 and 10% longer.)
+template <int MODE, bool FP8, int R>
+__global__ void __launch_bounds__(512, 2) k_expert_wide(ExpertArgs a, int cols) {
+    constexpr int NW = 8, BQ = 256, BP = 256, NQ = 4, NP = 8, SB = 128, kUnit = 128 * SB;
+    constexpr bool QA = MODE != kDw, PA = MODE == kForward;
+    __shared__ __align__(1024) char smem[R * kUnit];
+    __shared__ float sxs[2][FP8 ? BQ * kBlocks : 1], sws[2][FP8 ? kWave : 1];
+    const int lane = lane_id(), wave = uniform(threadIdx.x / kWave);
+    const int wq = wave % 4 * 64, wp = wave / 4 * 64;  // columns wp .. and 128 + wp ..
+    const bool gated = MODE == kForward && a.act == kActSwiglu, second = wave >= 4;
+    Tile t;
+    if (!find<MODE, FP8, BQ, BP>(a, cols, t)) return;
+
+    Loader<QA, 128, NW, SB> l0, l1;
+    Loader<PA, 128, NW, SB> l2, l3;
+    l0.init(t.q, t.pitchq, min(t.nq, 128), false, wave, lane);
+    l1.init(t.q + (QA ? 128 * (int64_t)t.pitchq : 256), t.pitchq, t.nq - 128, false, wave, lane);
+    const int ph = gated ? 64 : 128;
+    l2.init(t.p, t.pitchp, min(t.np, ph), gated, wave, lane);
+    l3.init(t.p + (PA ? ph * (int64_t)t.pitchp : 256), t.pitchp, t.np - ph, gated, wave, lane);
+    if (gated && wave / 2 % 2) {  // a wave's loads are all the gate's or all the up projection's
+        l2.at += (int64_t)a.N * t.pitchp;
+        l3.at += (int64_t)a.N * t.pitchp;
+    }
+    Reader<QA, 128, SB> rq;
+    Reader<PA, 128, SB> rp;
+    rq.init(wq % 128, lane);
+    rp.init(wp, lane);
+
+    typename Sum<FP8>::type acc[NP][NQ];
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
+
+    constexpr int EL = FP8 ? 1 : 2, kPerStep = SB / EL;
+    const int steps = (t.K + kPerStep - 1) / kPerStep;
+    // Unit 4 s + kind into place `at` of the ring.
+    auto issue = [&](int s, int kind, int at) {
+        const int left = t.K - s * kPerStep, lq = QA ? left / (16 / EL) : left, lp = PA ? left / (16 / EL) : left;
+        char *to = smem + at * kUnit;
+        if constexpr (FP8)
+            if (kind == 0 && s % kBlocks == 0 && s < steps) load_scales<BQ, NW>(a, t, sxs, sws, gated, s, wave, lane);
+        if (kind == 0) l0.issue(to, wave, lq);
+        else if (kind == 1) l1.issue(to, wave, lq);
+        else if (kind == 2) l2.issue(to, wave, lp);
+        else l3.issue(to, wave, lp);
+    };
+    auto wrap = [](int at) { return at >= R ? at - R : at; };
+    auto turn = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Loads end in order: a unit's are done when those of the R - 4 after it
+    // may be out.  Every wave waits for its own before the barrier after which
+    // the first half reads them.
+    constexpr int kLanded = (R - 4) * 2;
+    static_assert(l0.kLoads == 2 && l2.kLoads == 2 && kLanded < kAnyLoads, "two loads per unit");
+    const int up_from = ((a.N + t.p0) / 128 + 1) * 128 - a.N - t.p0;  // gated: up columns from here on take the third scale
+    if (steps > 0) {
+#pragma unroll
+        for (int u = 0; u < R - 1; ++u) issue(u / 4, u % 4, u);
+        __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
+        asm volatile("" ::: "memory");
+    }
+    turn();
+    if (second) turn();
+    int at = 0;  // place of the step's unit 0
+    for (int s = 0; s < steps; ++s) {
+        const char *sq = smem + wrap(at + wave % 4 / 2) * kUnit;
+        bf16x8 fq[NQ][2];
+        float xs[NQ];
+        f32x4 ws;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const char *sp = smem + wrap(at + 2 + h) * kUnit;
+            bf16x8 fp[NP / 2][2];
+            asm volatile("" ::: "memory");
+            if (h == 0) {
+                if (FP8) ws = w_scales(sws[s / kBlocks % 2], s);
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) {
+                    if (FP8) xs[j] = x_scale(sxs[s / kBlocks % 2], wq + j * 16 + lane % 16, s);
+                    fq[j][0] = rq.read(sq, j, 0);
+                    fq[j][1] = rq.read(sq, j, 1);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NP / 2; ++i) {
+                fp[i][0] = rp.read(sp, i, 0);
+                fp[i][1] = rp.read(sp, i, 1);
+            }
+            if (h == 0) {
+                issue(s + (R - 1) / 4, (R - 1) % 4, wrap(at + R - 1));
+            } else {
+                issue(s + R / 4, R % 4, at);
+                issue(s + (R + 1) / 4, (R + 1) % 4, wrap(at + 1));
+                issue(s + (R + 2) / 4, (R + 2) % 4, wrap(at + 2));
+            }
+            asm volatile("" ::: "memory");
+            if (second) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, 0));
+            else __builtin_amdgcn_s_waitcnt(wait_for(kAnyLoads, 0));
+            turn();
+            __builtin_amdgcn_s_setprio(1);
+            if constexpr (FP8) {
+                // Two products, and the scaling of the two before, at a time.
+                constexpr int kPairs = NP / 2 * NQ / 2;
+                f32x4 part[2][2];
+#pragma unroll
+                for (int u = 0; u <= kPairs; ++u) {
+#pragma unroll
+                    for (int v = 0; v < 2 && u < kPairs; ++v) {
+                        const int i = u * 2 / NQ, j = u * 2 % NQ + v;
+                        part[u % 2][v] = mfma8(join(fp[i][0], fp[i][1]), join(fq[j][0], fq[j][1]));
+                    }
+#pragma unroll
+                    for (int v = 0; v < 2 && u > 0; ++v) {
+                        const int i = (u - 1) * 2 / NQ, j = (u - 1) * 2 % NQ + v;
+                        const int c = (h * 128 + wp) / 2 + i / 2 * 16 + lane / 16 * 4;
+                        const float up = c < up_from ? ws[1] : ws[2];
+                        const float wsc = gated ? (i % 2 ? up : ws[0]) : ws[h];
+                        add_scaled(acc[h * (NP / 2) + i][j], part[(u - 1) % 2][v], xs[j] * wsc);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int i = 0; i < NP / 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j)
+                            acc[h * (NP / 2) + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                fp[i][kk], fq[j][kk], acc[h * (NP / 2) + i][j], 0, 0, 0);
+            }
+            __builtin_amdgcn_s_setprio(0);
+            asm volatile("" ::: "memory");
+            if (!second) __builtin_amdgcn_s_waitcnt(wait_for(kLanded, kAnyLds));
+            turn();
+        }
+        at = wrap(at + 4);
+    }
+    if (!second) turn();
+    static_assert((MODE == kForward ? 128 * BP * 4 : BQ * BP * 2) <= R * kUnit, "LDS");
+    put_tile<MODE, BQ, BP, NW, NP, NQ, true>(a, smem, acc, t, wq, wp, lane);
 }
 
 // Gradient of the pre-activation, bf16, and the columns' sums of its unrounded
@@ -707,15 +806,32 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 int64_t row_tiles(const ExpertArgs &a, int size) { return expert_row_tiles(a.rows, a.E, size); }
 
+template <int MODE>
+int64_t count_blocks(const ExpertArgs &a, int BQ, int BP, int threads, int *cols) {
+    const bool gated = MODE == kForward && a.act == kActSwiglu;
+    *cols = ceil_div(MODE == kForward ? a.N : a.I, gated ? BP / 2 : BP);
+    const int64_t tiles = (MODE == kDw ? (int64_t)ceil_div(a.Nw, BQ) * a.E : row_tiles(a, BQ)) * *cols;
+    const int64_t blocks = (tiles + kXcds * kPatch - 1) / (kXcds * kPatch) * (kXcds * kPatch);
+    return blocks > 4294967295ll / threads ? 0 : blocks;
+}
+
 template <int MODE, bool FP8, int BQ, int BP, int WQ, int WP, int SB, int NST>
 hipError_t run_tile(const ExpertArgs &a, hipStream_t st) {
-    const bool gated = MODE == kForward && a.act == kActSwiglu;
-    const int64_t cols = ceil_div(MODE == kForward ? a.N : a.I, gated ? BP / 2 : BP);
-    const int64_t tiles = MODE == kDw ? (int64_t)ceil_div(a.Nw, BQ) * a.E : row_tiles(a, BQ);
-    const int64_t blocks = (tiles * cols + kXcds * kPatch - 1) / (kXcds * kPatch) * (kXcds * kPatch);
-    if (blocks > 4294967295ll / (WQ * WP * kWave)) return hipErrorInvalidValue;
+    int cols;
+    const int64_t blocks = count_blocks<MODE>(a, BQ, BP, WQ * WP * kWave, &cols);
+    if (!blocks) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_expert_tile<MODE, FP8, BQ, BP, WQ, WP, SB, NST>), dim3((uint32_t)blocks), dim3(WQ * WP * kWave),
-                       0, st, a, (int)cols);
+                       0, st, a, cols);
+    return hipGetLastError();
+}
+
+template <int MODE, bool FP8>
+hipError_t run_wide(const ExpertArgs &a, hipStream_t st) {
+    int cols;
+    const int64_t blocks = count_blocks<MODE>(a, 256, 256, 512, &cols);
+    if (!blocks) return hipErrorInvalidValue;
+    // All of LDS; with fp8 the scales take the room of two units.
+    hipLaunchKernelGGL((k_expert_wide<MODE, FP8, FP8 ? 8 : 10>), dim3((uint32_t)blocks), dim3(512), 0, st, a, cols);
     return hipGetLastError();
 }
 
@@ -753,7 +869,7 @@ hipError_t run(const ExpertArgs &a, hipStream_t st) {
         }
     }
     if (c128 < c256) return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
-    return run_tile<MODE, FP8, 256, 256, 4, 2, FP8 ? 128 : 64, FP8 ? 2 : 5>(a, st);
+    return run_wide<MODE, FP8>(a, st);
 }
 
 }  // namespace
