@@ -137,17 +137,17 @@ __device__ __forceinline__ bool place_tile(int b, int rows, int cols, int &row, 
 }
 
 // The workgroup's tile of `size` rows of an expert's segment and its column.
-__device__ __forceinline__ bool locate(const ExpertArgs &a, int size, int cols, Segment &g, int &col) {
+__device__ __forceinline__ bool locate(const ExpertArgs &a, int block, int size, int cols, Segment &g, int &col) {
     int row;
     if (a.E > kWave) {
-        if (!place_tile(blockIdx.x, count_tiles(a.base, a.E, a.rows, size), cols, row, col)) return false;
+        if (!place_tile(block, count_tiles(a.base, a.E, a.rows, size), cols, row, col)) return false;
         g = find_tile(a.base, a.E, a.rows, size, row);
         return g.e >= 0;
     }
     const int lane = lane_id();
     g = lane < a.E ? segment_of(a.base, lane, a.rows) : Segment{lane, 0, 0};
     const int mine = (g.n + size - 1) / size, incl = wave_scan(mine);
-    if (!place_tile(blockIdx.x, read_lane(incl, kWave - 1), cols, row, col)) return false;
+    if (!place_tile(block, read_lane(incl, kWave - 1), cols, row, col)) return false;
     const int o = __builtin_ctzll(ballot(incl > row));
     const int at = row - (read_lane(incl, o) - read_lane(mine, o));
     const int left = read_lane(g.n, o) - at * size;
@@ -308,7 +308,7 @@ struct Tile {
 };
 
 template <int MODE, bool FP8, int BQ, int BP>
-__device__ __forceinline__ bool find(const ExpertArgs &a, int cols, Tile &t) {
+__device__ __forceinline__ bool find(const ExpertArgs &a, int block, int cols, Tile &t) {
     constexpr int EL = FP8 ? 1 : 2;
     int tcol;
     Segment g;
@@ -316,10 +316,10 @@ __device__ __forceinline__ bool find(const ExpertArgs &a, int cols, Tile &t) {
     if (MODE == kDw) {
         const int per = (a.Nw + BQ - 1) / BQ;
         int trow;
-        if (!place_tile(blockIdx.x, per * a.E, cols, trow, tcol)) return false;
+        if (!place_tile(block, per * a.E, cols, trow, tcol)) return false;
         g = segment_of(a.base, trow / per, a.rows);
         t.q0 = trow % per * BQ;
-    } else if (!locate(a, BQ, cols, g, tcol)) {
+    } else if (!locate(a, block, BQ, cols, g, tcol)) {
         return false;
     }
     const bool gated = MODE == kForward && a.act == kActSwiglu;
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
     const int wq = wave % WQ * (BQ / WQ), wp = wave / WQ * (BP / WP);
     const bool gated = MODE == kForward && a.act == kActSwiglu;
     Tile t;
-    if (!find<MODE, FP8, BQ, BP>(a, cols, t)) return;
+    if (!find<MODE, FP8, BQ, BP>(a, blockIdx.x, cols, t)) return;
 
     Loader<QA, BQ, NW, SB> lq;
     Loader<PA, BP, NW, SB> lp;
@@ -553,17 +553,17 @@ __global__ void __launch_bounds__(WQ *WP *kWave, 2) k_expert_tile(ExpertArgs a, 
 // its second, two loads per wave each.  So R - 4 units are on their way at
 // every wait, 6 to 10 turns before they are read.  (In stages of whole steps,
 // or of half lines, the same product took 15 and 10% longer.)
+constexpr int kUnit = 128 * 128;
 template <int MODE, bool FP8, int R>
-__global__ void __launch_bounds__(512, 2) k_expert_wide(ExpertArgs a, int cols) {
-    constexpr int NW = 8, BQ = 256, BP = 256, NQ = 4, NP = 8, SB = 128, kUnit = 128 * SB;
+__device__ __forceinline__ void wide_tile(const ExpertArgs &a, int block, int cols, char *smem, float (*sxs)[256 * kBlocks],
+                                          float (*sws)[kWave]) {
+    constexpr int NW = 8, BQ = 256, BP = 256, NQ = 4, NP = 8, SB = 128;
     constexpr bool QA = MODE != kDw, PA = MODE == kForward;
-    __shared__ __align__(1024) char smem[R * kUnit];
-    __shared__ float sxs[2][FP8 ? BQ * kBlocks : 1], sws[2][FP8 ? kWave : 1];
     const int lane = lane_id(), wave = uniform(threadIdx.x / kWave);
     const int wq = wave % 4 * 64, wp = wave / 4 * 64;  // columns wp .. and 128 + wp ..
     const bool gated = MODE == kForward && a.act == kActSwiglu, second = wave >= 4;
     Tile t;
-    if (!find<MODE, FP8, BQ, BP>(a, cols, t)) return;
+    if (!find<MODE, FP8, BQ, BP>(a, block, cols, t)) return;
 
     Loader<QA, 128, NW, SB> l0, l1;
     Loader<PA, 128, NW, SB> l2, l3;
@@ -660,23 +660,26 @@ __global__ void __launch_bounds__(512, 2) k_expert_wide(ExpertArgs a, int cols) 
             turn();
             __builtin_amdgcn_s_setprio(1);
             if constexpr (FP8) {
-                // Two products, and the scaling of the two before, at a time.
-                constexpr int kPairs = NP / 2 * NQ / 2;
-                f32x4 part[2][2];
+                // Two products at a time, then the scaling of the pair two
+                // before, which is ready by then: closer together the matrix
+                // unit idles until the scaling is done (595 us, 4096 tokens).
+                constexpr int kPairs = NP / 2 * NQ / 2, kAfter = 2;
+                f32x4 part[kAfter + 1][2];
 #pragma unroll
-                for (int u = 0; u <= kPairs; ++u) {
+                for (int u = 0; u < kPairs + kAfter; ++u) {
 #pragma unroll
                     for (int v = 0; v < 2 && u < kPairs; ++v) {
                         const int i = u * 2 / NQ, j = u * 2 % NQ + v;
-                        part[u % 2][v] = mfma8(join(fp[i][0], fp[i][1]), join(fq[j][0], fq[j][1]));
+                        part[u % (kAfter + 1)][v] = mfma8(join(fp[i][0], fp[i][1]), join(fq[j][0], fq[j][1]));
                     }
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int v = 0; v < 2 && u > 0; ++v) {
-                        const int i = (u - 1) * 2 / NQ, j = (u - 1) * 2 % NQ + v;
+                    for (int v = 0; v < 2 && u >= kAfter; ++v) {
+                        const int o = u - kAfter, i = o * 2 / NQ, j = o * 2 % NQ + v;
                         const int c = (h * 128 + wp) / 2 + i / 2 * 16 + lane / 16 * 4;
                         const float up = c < up_from ? ws[1] : ws[2];
                         const float wsc = gated ? (i % 2 ? up : ws[0]) : ws[h];
-                        add_scaled(acc[h * (NP / 2) + i][j], part[(u - 1) % 2][v], xs[j] * wsc);
+                        add_scaled(acc[h * (NP / 2) + i][j], part[o % (kAfter + 1)][v], xs[j] * wsc);
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -700,6 +703,25 @@ __global__ void __launch_bounds__(512, 2) k_expert_wide(ExpertArgs a, int cols) 
     if (!second) turn();
     static_assert((MODE == kForward ? 128 * BP * 4 : BQ * BP * 2) <= R * kUnit, "LDS");
     put_tile<MODE, BQ, BP, NW, NP, NQ, true>(a, smem, acc, t, wq, wp, lane);
+}
+
+// All of LDS; with fp8 the scales take the room of two units.
+template <bool FP8>
+__global__ void __launch_bounds__(512, 2) k_expert_wide(ExpertArgs a, int cols) {
+    __shared__ __align__(1024) char smem[(FP8 ? 8 : 10) * kUnit];
+    __shared__ float sxs[FP8 ? 2 : 1][256 * kBlocks / (FP8 ? 1 : 256 * kBlocks)], sws[FP8 ? 2 : 1][FP8 ? kWave : 1];
+    wide_tile<kForward, FP8, FP8 ? 8 : 10>(a, blockIdx.x, cols, smem, reinterpret_cast<float(*)[256 * kBlocks]>(sxs),
+                                           reinterpret_cast<float(*)[kWave]>(sws));
+}
+
+// The gradients' tiles of 256 x 256 in one launch, those of d_x first (blocks
+// below `dx`): the tiles of d_w, with few steps each, fill what the last ones of
+// d_x leave idle.
+__global__ void __launch_bounds__(512, 2) k_expert_wide_back(ExpertArgs a, int cols, int dx) {
+    __shared__ __align__(1024) char smem[10 * kUnit];
+    const int block = blockIdx.x;
+    if (block < dx) wide_tile<kDx, false, 10>(a, block, cols, smem, nullptr, nullptr);
+    else wide_tile<kDw, false, 10>(a, block - dx, cols, smem, nullptr, nullptr);
 }
 
 // Gradient of the pre-activation, bf16, and the columns' sums of its unrounded
@@ -829,58 +851,109 @@ hipError_t run_tile(const ExpertArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int MODE, bool FP8>
+template <bool FP8>
 hipError_t run_wide(const ExpertArgs &a, hipStream_t st) {
     int cols;
-    const int64_t blocks = count_blocks<MODE>(a, 256, 256, 512, &cols);
+    const int64_t blocks = count_blocks<kForward>(a, 256, 256, 512, &cols);
     if (!blocks) return hipErrorInvalidValue;
-    // All of LDS; with fp8 the scales take the room of two units.
-    hipLaunchKernelGGL((k_expert_wide<MODE, FP8, FP8 ? 8 : 10>), dim3((uint32_t)blocks), dim3(512), 0, st, a, cols);
+    hipLaunchKernelGGL(k_expert_wide<FP8>, dim3((uint32_t)blocks), dim3(512), 0, st, a, cols);
     return hipGetLastError();
 }
 
-// Microseconds that a product of `steps` 128-byte steps takes in tiles of BQ x
-// BP: so many rounds of as many tiles as the card holds at once, each with a
+// The gradients in wide tiles, one or both.
+hipError_t run_wide_back(const ExpertArgs &a, bool d_x, bool d_w, hipStream_t st) {
+    int cols;
+    const int64_t bx = count_blocks<kDx>(a, 256, 256, 512, &cols), bw = count_blocks<kDw>(a, 256, 256, 512, &cols);
+    const int64_t blocks = (d_x ? bx : 0) + (d_w ? bw : 0);
+    if (!bx || !bw || blocks > 4294967295ll / 512) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(k_expert_wide_back, dim3((uint32_t)blocks), dim3(512), 0, st, a, cols, d_x ? (int)bx : 0);
+    return hipGetLastError();
+}
+
+// Microseconds that a product of `steps` 128-byte steps takes in tiles of one
+// size: so many rounds of as many tiles as the card holds at once, each with a
 // start and an epilogue; a step takes `full` in a round that fills the card,
-// `least` with one tile alone.  Measured on 16 experts of 4 to 1024 rows, 2048
-// to 2 x 1024 and 4096 to 2048 (at 192 rows: 72 us in 32-row tiles, 38 in
-// 64-row, 34 in 128-row, 46 in 256-row tiles; at 1024 rows 302, 160, 131, 116).
-double tile_cost(const ExpertArgs &a, bool dw, int columns, int BQ, int BP, int slots, int steps, double start,
-                 double least, double full) {
+// `least` with one tile alone.  Fitted to 16 experts of 4 to 1024 rows, 2048 to
+// 2 x 1024 and 4096 to 2048 features.  Forward, 4096 to 2048, at 4 rows: 40 us
+// in 32-row tiles, 77 in 256-row tiles; at 128: 64 in 64-row, 66 in 128-row, 83
+// in 256-row; at 256: 88 in 128-row, 90 in 256-row; at 1024: 273 in 128-row, 206
+// in 256-row tiles.
+template <int MODE, bool FP8>
+double cost(const ExpertArgs &a, int BQ, int BP, int slots, double start, double least, double full) {
     const int64_t some = a.rows < a.E ? a.rows : a.E;
     int64_t tiles = a.rows / BQ + some / 2;  // on average half a tile is missing from each expert's last
-    tiles = dw ? (int64_t)a.E * ceil_div(a.Nw, BQ) : (tiles > some ? tiles : some);
-    tiles *= ceil_div(columns, BP);
+    tiles = MODE == kDw ? (int64_t)a.E * ceil_div(a.Nw, BQ) : (tiles > some ? tiles : some);
+    tiles *= ceil_div(MODE == kForward ? a.Nw : a.I, BP);
+    const int steps = ceil_div(MODE == kForward ? a.I : (MODE == kDw ? a.rows / a.E : a.Nw), FP8 ? 128 : 64);
     const int64_t rounds = tiles / slots, rest = tiles % slots;
     return rounds * (start + steps * full) + (rest ? start + steps * (least + (full - least) * rest / slots) : 0.0);
 }
-
 template <int MODE, bool FP8>
-hipError_t run(const ExpertArgs &a, hipStream_t st) {
-    constexpr bool F = MODE == kForward, W = MODE == kDw;
-    const int K = F ? a.I : (W ? (int)(a.rows / a.E) : a.Nw), steps = ceil_div(K, FP8 ? 128 : 64);
-    const int columns = F ? a.Nw : a.I;
-    const double c256 = tile_cost(a, W, columns, 256, 256, 256, steps, 8, 1.1, 1.85);
-    const double c128 = tile_cost(a, W, columns, 128, 128, 512, steps, 5, 0.55, 1.15);
-    if constexpr (!W) {
-        const double c64 = tile_cost(a, W, columns, 64, 128, 512, steps, 3.5, 0.35, 0.7);
-        const double c32 = F ? tile_cost(a, W, columns, 32, 64, 512, steps, 3, 0.2, 0.32)
-                             : tile_cost(a, W, columns, 32, 128, 512, steps, 3, 0.3, 0.69);
-        const double best = c64 < c32 ? c64 : c32;
-        if (best <= c128 && best <= c256) {
-            if (c64 < c32) return run_tile<MODE, FP8, 64, 128, 2, 2, 128, 3>(a, st);
+double cost_wide(const ExpertArgs &a) {
+    if (MODE == kDw) return cost<MODE, FP8>(a, 256, 256, 256, 7.7, 1.1, 1.43);
+    return FP8 ? cost<MODE, FP8>(a, 256, 256, 256, 5, 1.55, 2.05) : cost<MODE, FP8>(a, 256, 256, 256, 5, 1.15, 1.55);
+}
+template <int MODE, bool FP8>
+double cost_128(const ExpertArgs &a) {
+    if (MODE == kDw) return cost<MODE, FP8>(a, 128, 128, 512, 3.4, 0.6, 1.0);
+    return FP8 ? cost<MODE, FP8>(a, 128, 128, 512, 5, 1.15, 1.3) : cost<MODE, FP8>(a, 128, 128, 512, 5, 0.6, 1.0);
+}
+template <int MODE, bool FP8>
+double cost_64(const ExpertArgs &a) {
+    return FP8 ? cost<MODE, FP8>(a, 64, 128, 512, 3.5, 0.9, 1.1) : cost<MODE, FP8>(a, 64, 128, 512, 3.5, 0.4, 0.72);
+}
+template <int MODE, bool FP8>
+double cost_32(const ExpertArgs &a) {
+    if (MODE != kForward) return cost<MODE, FP8>(a, 32, 128, 512, 3, 0.3, 0.69);
+    return FP8 ? cost<MODE, FP8>(a, 32, 64, 512, 3, 0.65, 0.7) : cost<MODE, FP8>(a, 32, 64, 512, 3, 0.2, 0.32);
+}
+
+// The product in the cheapest tiles below 256 x 256, and its cost.
+template <int MODE, bool FP8>
+double cost_small(const ExpertArgs &a) {
+    double c = cost_128<MODE, FP8>(a);
+    if (MODE == kDw) return c;
+    const double c64 = cost_64<MODE, FP8>(a), c32 = cost_32<MODE, FP8>(a);
+    c = c64 < c ? c64 : c;
+    return c32 < c ? c32 : c;
+}
+template <int MODE, bool FP8>
+hipError_t run_small(const ExpertArgs &a, hipStream_t st) {
+    constexpr bool F = MODE == kForward;
+    if constexpr (MODE != kDw) {
+        const double c = cost_small<MODE, FP8>(a);
+        if (c == cost_32<MODE, FP8>(a))
             return run_tile<MODE, FP8, 32, F ? 64 : 128, F ? 2 : 1, F ? 2 : 4, 128, F ? 6 : 4>(a, st);
-        }
+        if (c == cost_64<MODE, FP8>(a)) return run_tile<MODE, FP8, 64, 128, 2, 2, 128, 3>(a, st);
     }
-    if (c128 < c256) return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
-    return run_wide<MODE, FP8>(a, st);
+    return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
+}
+
+template <bool FP8>
+hipError_t run_forward(const ExpertArgs &a, hipStream_t st) {
+    if (cost_wide<kForward, FP8>(a) < cost_small<kForward, FP8>(a)) return run_wide<FP8>(a, st);
+    return run_small<kForward, FP8>(a, st);
+}
+
+// Both gradients go in one launch where both are best in wide tiles (565 us in
+// two, 555 in one; 2331 rows of 24 experts, d_x best in 64-row tiles: 73 in two,
+// 82 in one).
+hipError_t run_back(const ExpertArgs &a, hipStream_t st) {
+    const bool x = a.d_x && a.rows > 0, w = a.d_w;
+    const bool wide_x = x && cost_wide<kDx, false>(a) < cost_small<kDx, false>(a);
+    const bool wide_w = w && cost_wide<kDw, false>(a) < cost_small<kDw, false>(a);
+    hipError_t rc = hipSuccess;
+    if (wide_x || wide_w) rc = run_wide_back(a, wide_x, wide_w, st);
+    if (rc == hipSuccess && x && !wide_x) rc = run_small<kDx, false>(a, st);
+    if (rc == hipSuccess && w && !wide_w) rc = run_small<kDw, false>(a, st);
+    return rc;
 }
 
 }  // namespace
 
 hipError_t launch_expert(const ExpertArgs &a, hipStream_t st) {
     if (a.rows == 0) return hipSuccess;
-    return a.fp8 ? run<kForward, true>(a, st) : run<kForward, false>(a, st);
+    return a.fp8 ? run_forward<true>(a, st) : run_forward<false>(a, st);
 }
 
 hipError_t launch_expert_backward(const ExpertArgs &args, hipStream_t st) {
@@ -901,8 +974,7 @@ hipError_t launch_expert_backward(const ExpertArgs &args, hipStream_t st) {
         hipLaunchKernelGGL(k_expert_bias_sum, dim3(ceil_div(a.Nw, kWave), a.E), dim3(kThreads), 0, st, a);
         if ((rc = hipGetLastError()) != hipSuccess) return rc;
     }
-    if (a.d_x && a.rows > 0 && (rc = run<kDx, false>(a, st)) != hipSuccess) return rc;
-    return a.d_w ? run<kDw, false>(a, st) : rc;
+    return run_back(a, st);
 }
 
 }  // namespace ep
