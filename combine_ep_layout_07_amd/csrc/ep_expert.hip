@@ -76,7 +76,7 @@ struct Loader {
         step = ALONG ? SB : SB / 2 * (int64_t)pitch;
         off = ALONG || c * 8 < rows ? (gated ? r / 32 * 16 + r % 16 : r) * pitch + c * 16 : kOutside;
         apart = NW * kRows / (gated ? 2 : 1) * pitch;
-        bytes = !ALONG ? kOutside : (rows > 0 ? (rows - 1) * pitch + SB : 0);
+        bytes = !ALONG ? kOutside : (rows > 0 ? (rows - 1) * pitch + (pitch < SB ? pitch : SB) : 0);
         place = ALONG ? c : r;
     }
     // Issues the loads of one stage; `left` chunks (ALONG) or rows of k remain
@@ -148,7 +148,9 @@ __device__ __forceinline__ bool locate(const ExpertArgs &a, int block, int size,
     g = lane < a.E ? segment_of(a.base, lane, a.rows) : Segment{lane, 0, 0};
     const int mine = (g.n + size - 1) / size, incl = wave_scan(mine);
     if (!place_tile(block, read_lane(incl, kWave - 1), cols, row, col)) return false;
-    const int o = __builtin_ctzll(ballot(incl > row));
+    const uint64_t past = ballot(incl > row);
+    if (!past) return false;
+    const int o = __builtin_ctzll(past);
     const int at = row - (read_lane(incl, o) - read_lane(mine, o));
     const int left = read_lane(g.n, o) - at * size;
     g = {o, (int64_t)read_lane((int)g.r0, o) + (int64_t)at * size, left < size ? left : size};

@@ -319,6 +319,70 @@ def terms64(act, p, d, N):
     return torch.cat([d.abs() * p[:, N:].abs() * (1 + p[:, :N].abs()), d.abs() * p[:, :N].abs()], 1)
 
 
+# Sizes at which the tiles of 256 x 256 and of 128 x 128 are the cheapest; 64-bit products on the GPU.
+LARGE = [([3001, 0, 1999], 2056, 1032, "swiglu"), ([1500, 2500], 520, 1032, "gelu"), ([1500, 2500], 1032, 520, "silu")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,I,N,act", LARGE)
+def test_large(counts, I, N, act):
+    print(f"[expert_mm large] {counts} I={I} N={N} {act}", flush=True)
+    base, rows, x, w, g = make(counts, I, N, act, 21, first=3)
+    E, Nw = len(counts), cols_of(N, act)
+    b = torch.randn((E, Nw), generator=g)
+    res = torch.randn((rows, N), generator=g).bfloat16()
+    d = torch.randn((rows, N), generator=g).bfloat16()
+    for t in (x, d):  # rows outside the segments
+        t[:base[0]] = float("nan")
+        t[base[-1]:] = float("inf")
+    xd, wd, bd, dd = x.cuda(), w.cuda(), b.cuda(), d.cuda()
+    bt = torch.tensor(base, dtype=torch.int32).cuda()
+    cfg = ep.make_expert_config(E, rows, I, N, activation=act)
+    out = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    pre = torch.full((rows, Nw), 7.0, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_mm(cfg, bt, xd, wd, out, bias=bd, residual=res.cuda(), pre=pre)
+    p, mag = (t.cpu() for t in product64(base, xd, wd, bd))
+    check_forward(base, out, pre, p, mag, I, N, act, res)
+    dx, dw, db = torch.full_like(xd, 7.0), torch.full_like(wd, 7.0), torch.empty((E, Nw), device="cuda")
+    ep.ep_expert_mm_backward(cfg, bt, xd, wd, dd, ep.alloc_expert_backward(cfg), pre=pre, d_x=dx, d_w=dw, d_bias=db)
+    assert (dx[:base[0]] == 7).all() and (dx[base[-1]:] == 7).all()
+    for e in range(E):
+        s = slice(int(base[e]), int(base[e + 1]))
+        n, pe, de = s.stop - s.start, pre[s].double(), dd[s].double()
+        grad = slope64(act, pe, de, N)
+        err = 16 * U * terms64(act, pe, de, N)
+        m = grad.abs() * (1 + H) + err
+        want, bound = grad @ wd[e].double(), (H + 2 * Nw * U) * (m @ wd[e].double().abs()) + err @ wd[e].double().abs()
+        assert (torch.abs(dx[s].double() - want) <= H * want.abs() + (1 + H) * bound).all()
+        assert n == 0 or (dx[s].double() - want).norm() <= 2 * H * want.norm()
+        xe = x[s].cuda().double()
+        want, bound = grad.T @ xe, (H + 2 * n * U) * (m.T @ xe.abs()) + err.T @ xe.abs()
+        assert (torch.abs(dw[e].double() - want) <= H * want.abs() + (1 + H) * bound).all()
+        assert n == 0 or (dw[e].double() - want).norm() <= 2 * H * want.norm()
+        assert (torch.abs(db[e].double() - grad.sum(0)) <= ((n + 16) * U * m + err).sum(0)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,I,N,act", [([3001, 0, 1999], 768, 1032, "swiglu"), ([3001, 0, 1999], 2432, 1040, "none"),
+                                            ([1500, 2500], 1024, 1032, "silu"), ([700, 1800], 1152, 520, "swiglu")])
+def test_large_fp8(counts, I, N, act):
+    print(f"[expert_mm large fp8] {counts} I={I} N={N} {act}", flush=True)
+    base, rows, x, w, g = make(counts, I, N, act, 22, first=1)
+    E, Nw = len(counts), cols_of(N, act)
+    x8, w8 = x.to(torch.float8_e4m3fn), (w.float() * I ** 0.5).to(torch.float8_e4m3fn)
+    xs = torch.exp(torch.randn((rows, I // 128), generator=g))
+    ws = torch.exp(torch.randn((E, -(-Nw // 128), I // 128), generator=g)) * I ** -0.5
+    out = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    kept = torch.full((rows, Nw), 7.0, dtype=torch.bfloat16, device="cuda")
+    cfg = ep.make_expert_config(E, rows, I, N, dtype="fp8", activation=act)
+    ep.ep_expert_mm(cfg, torch.tensor(base, dtype=torch.int32).cuda(), x8.cuda(), w8.cuda(), out, x_sf=xs.cuda(),
+                    w_sf=ws.cuda(), pre=kept)
+    x64 = x8.double() * xs.double().repeat_interleave(128, 1)
+    w64 = w8.double() * ws.double().repeat_interleave(128, 2).repeat_interleave(128, 1)[:, :Nw]
+    p, mag = (t.cpu() for t in product64(base, x64.cuda(), w64.cuda(), None))
+    check_forward(base, out, kept, p, mag, I + 4, N, act, None)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", ["none", "gelu", "silu", "swiglu"])
 def test_gradient_against_differences(act):
