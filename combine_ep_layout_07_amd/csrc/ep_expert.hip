@@ -184,11 +184,12 @@ __device__ __forceinline__ void load_float(const float *p, float (&v)[W]) {
 }
 
 // W neighbouring outputs from the biased fp32 sums `v` (and, gated, those of
-// the up projection): the kept pre-activation, activation and residual.
+// the up projection): the kept pre-activation, activation and residual; stored
+// where `in`.
 template <bool GATED, int W>
-__device__ __forceinline__ void finish(const ExpertArgs &a, int64_t r, int c, float (&v)[W], const float (&up)[W],
+__device__ __forceinline__ void finish(const ExpertArgs &a, bool in, int64_t r, int c, float (&v)[W], const float (&up)[W],
                                        const uint32_t (&res)[W / 2]) {
-    if (a.pre) {
+    if (a.pre && in) {
         uint16_t *to = a.pre + r * a.Nw + c;
         store_bf16<W>(to, v);
         if (GATED) store_bf16<W>(to + a.N, up);
@@ -210,7 +211,7 @@ __device__ __forceinline__ void finish(const ExpertArgs &a, int64_t r, int c, fl
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += i % 2 ? bf16_hi(res[i / 2]) : bf16_lo(res[i / 2]);
     }
-    store_bf16<W>(a.out + r * a.N + c, v);
+    if (in) store_bf16<W>(a.out + r * a.N + c, v);
 }
 
 __device__ __forceinline__ void lds_barrier() {
@@ -268,8 +269,9 @@ __device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, AC
         lds_barrier();
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            const int q = q0 + k * kApart;
-            if (q >= kRowsPer || h * kRowsPer + q >= nq || c >= a.N) continue;
+            // No branch around the arithmetic, so that items overlap.
+            const int q = kItems * kApart > kRowsPer ? min(q0 + k * kApart, kRowsPer - 1) : q0 + k * kApart;
+            const bool in = q0 + k * kApart < kRowsPer && h * kRowsPer + q < nq && c < a.N;
             const char *row = smem + q * BP * 4;
             float v[8], up[8];
 #pragma unroll
@@ -280,7 +282,7 @@ __device__ __forceinline__ void forward_rows(const ExpertArgs &a, char *smem, AC
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[4 * i + r] = l[r] + bv[4 * i + r], up[4 * i + r] = u[r] + bu[4 * i + r];
             }
-            finish<GATED, 8>(a, r0 + h * kRowsPer + q, c, v, up, res[k]);
+            finish<GATED, 8>(a, in, r0 + h * kRowsPer + q, c, v, up, res[k]);
         }
     }
 }
