@@ -160,7 +160,7 @@ def ep_query_sizes(cfg: EpConfig) -> EpSizes:
 # pointers and streams (the argtypes convert them), one size property.
 def _stream(stream) -> int:
     if stream is None:  # the handle alone: a Stream object takes 2.5 us of a call's 8
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -493,19 +493,20 @@ def ep_query_expert_sizes(cfg: EpExpertConfig) -> EpExpertSizes:
     return sz
 
 
-def _expert_sizes(cfg: EpExpertConfig) -> EpExpertSizes:
-    """ep_query_expert_sizes, kept on cfg with the bytes it was computed from."""
+def _expert_sizes(cfg: EpExpertConfig) -> tuple:
+    """The fields of ep_query_expert_sizes in order, kept on cfg with the bytes they were computed from."""
     key = bytes(cfg)
     memo = getattr(cfg, "_sizes_memo", None)
     if memo is None or memo[0] != key:
-        memo = (key, ep_query_expert_sizes(cfg))
+        sz = ep_query_expert_sizes(cfg)
+        memo = (key, tuple(getattr(sz, name) for name, _ in EpExpertSizes._fields_))
         cfg._sizes_memo = memo
     return memo[1]
 
 
 def alloc_expert_backward(cfg: EpExpertConfig, device="cuda") -> torch.Tensor:
     """Scratch of ep_expert_mm_backward; one that is not in use may serve any call of the same configuration."""
-    return torch.empty(max(1, int(_expert_sizes(cfg).backward_scratch)), dtype=torch.uint8, device=device)
+    return torch.empty(max(1, _expert_sizes(cfg)[7]), dtype=torch.uint8, device=device)
 
 
 def _base_ptr(cfg: EpExpertConfig, t: torch.Tensor) -> Optional[int]:
@@ -529,15 +530,15 @@ def ep_expert_mm(cfg: EpExpertConfig, expert_base: torch.Tensor, x: torch.Tensor
                  bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
                  pre: Optional[torch.Tensor] = None, stream=None) -> None:
     """out = act(x W_e^T + bias) + residual over rows grouped by expert; ``pre`` keeps the pre-activation."""
-    sz = _expert_sizes(cfg)
+    nx, nx_sf, nw, nw_sf, nbias, nout, npre, _ = _expert_sizes(cfg)
     el = 1 if cfg.x_dtype == EP_DTYPE_FP8_E4M3FN else 2
     _check_elem(x, "x", el)
     _check_elem(w, "w", el)
     _check_elem(out, "out", 2)
     rc = _lib.ep_expert_mm(
-        ctypes.byref(cfg), _base_ptr(cfg, expert_base), _ptr(x, "x", sz.x), _opt(x_sf, "x_sf", sz.x_sf, 4),
-        _ptr(w, "w", sz.w), _opt(w_sf, "w_sf", sz.w_sf, 4), _opt(bias, "bias", sz.bias, 4),
-        _opt(residual, "residual", sz.out, 2), _ptr(out, "out", sz.out), _opt(pre, "pre", sz.pre, 2), _stream(stream))
+        ctypes.byref(cfg), _base_ptr(cfg, expert_base), _ptr(x, "x", nx), _opt(x_sf, "x_sf", nx_sf, 4),
+        _ptr(w, "w", nw), _opt(w_sf, "w_sf", nw_sf, 4), _opt(bias, "bias", nbias, 4),
+        _opt(residual, "residual", nout, 2), _ptr(out, "out", nout), _opt(pre, "pre", npre, 2), _stream(stream))
     if rc != EP_OK:
         raise EpError(rc, "ep_expert_mm")
 
@@ -547,13 +548,13 @@ def ep_expert_mm_backward(cfg: EpExpertConfig, expert_base: torch.Tensor, x: Opt
                           d_x: Optional[torch.Tensor] = None, d_w: Optional[torch.Tensor] = None,
                           d_bias: Optional[torch.Tensor] = None, stream=None) -> None:
     """Gradients of a bf16 ep_expert_mm, each optional, from that of its output and the kept pre-activation."""
-    sz = _expert_sizes(cfg)
+    nx, _, nw, _, nbias, nout, npre, nscratch = _expert_sizes(cfg)
     _check_elem(w, "w", 2)
     _check_elem(d_out, "d_out", 2)
     rc = _lib.ep_expert_mm_backward(
-        ctypes.byref(cfg), _base_ptr(cfg, expert_base), _opt(x, "x", sz.x, 2), _ptr(w, "w", sz.w),
-        _opt(pre, "pre", sz.pre, 2), _ptr(d_out, "d_out", sz.out), _opt(d_x, "d_x", sz.x, 2),
-        _opt(d_w, "d_w", sz.w, 2), _opt(d_bias, "d_bias", sz.bias, 4),
-        _ptr(scratch, "scratch", sz.backward_scratch), _stream(stream))
+        ctypes.byref(cfg), _base_ptr(cfg, expert_base), _opt(x, "x", nx, 2), _ptr(w, "w", nw),
+        _opt(pre, "pre", npre, 2), _ptr(d_out, "d_out", nout), _opt(d_x, "d_x", nx, 2),
+        _opt(d_w, "d_w", nw, 2), _opt(d_bias, "d_bias", nbias, 4),
+        _ptr(scratch, "scratch", nscratch), _stream(stream))
     if rc != EP_OK:
         raise EpError(rc, "ep_expert_mm_backward")
