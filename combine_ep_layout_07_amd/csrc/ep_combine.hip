@@ -369,9 +369,10 @@ hipError_t launch_combine_backward(const CombineBackwardArgs &b, hipStream_t str
     const Shape &sh = b.c.sh;
     const int64_t n_tok = (int64_t)sh.S * sh.T;
     if (n_tok > 0) {
-        // A row of one pass of one wave stays with that wave; a longer one is
-        // split over the workgroup's four.
-        const bool wide = sh.H / 8 > kWave;
+        // A row of one or two passes of one wave stays with that wave; a longer
+        // one is split over the workgroup's four (4055 tokens, H = 664: 11 us and
+        // 20; 2000 tokens, H = 2048: 34 and 29).
+        const bool wide = sh.H / 8 > 2 * kWave;
         const int64_t want = wide ? n_tok : (n_tok + kWavesPerBlock - 1) / kWavesPerBlock;
         const int blocks = (int)(want < EP_COMBINE_MAX_BLOCKS ? want : EP_COMBINE_MAX_BLOCKS);
         if (wide) hipLaunchKernelGGL(k_combine_backward<kWavesPerBlock>, dim3(blocks), dim3(kThreads), 0, stream, b);

@@ -889,9 +889,11 @@ hipError_t run_rows(RouteArgs a, bool backward, int blocks, hipStream_t st) {
 
 // Several tokens per wave: from kManyTokens on, where there are waves enough
 // for the card either way (256 experts, top-8, forward: 4096 tokens 6.8 us with
-// a token per wave, 8.5 with four; 8192 10.5 and 9.2; 32768 35 and 19).
+// a token per wave, 8.5 with four; 8192 10.5 and 9.2; 32768 35 and 19), and
+// sooner with few experts, which leave a wave's lanes with one each (64 experts,
+// 6555 tokens, top-11 with a bias: 13.4 us).
 bool many_tokens(int S, int T, int E, int K) {
-    return (int64_t)S * T >= kManyTokens && E <= 512 && K < (E <= 256 ? 16 : 32);
+    return (int64_t)S * T >= (E <= 64 ? kManyTokens / 4 : kManyTokens) && E <= 512 && K < (E <= 256 ? 16 : 32);
 }
 
 }  // namespace
