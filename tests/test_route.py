@@ -379,6 +379,20 @@ def test_many_tokens(S, T, E, K, dtype, scoring):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("S,T,E,K", [(1, 1025, 48, 4), (3, 683, 100, 6), (1, 1500, 256, 8), (2, 600, 512, 11), (1, 1100, 700, 32),
+                                     (1, 2048, 64, 6), (2, 1031, 33, 15)])
+def test_between_few_and_many_tokens(S, T, E, K, dtype, scoring):
+    """A token per wave in large workgroups; several tokens per wave for few experts."""
+    rng = np.random.default_rng(S * 17 + T + E)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    mask = (rng.uniform(size=(S, T)) < 0.9).astype(np.uint8)
+    check(S, T, E, K, dtype, scoring, seed=5)
+    check(S, T, E, K, dtype, scoring, bias, mask, seed=6)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_many_tokens_with_near_ties(scoring, biased):
