@@ -161,7 +161,8 @@ def within(err, tol):
     assert not bad.any(), f"{bad.sum()} of {bad.size} outside; worst {(err / tol)[bad].max():.3g} of the tolerance"
 
 
-def check(S, T, E, K, dtype, scoring, bias=None, mask=None, logits=None, seed=0, scale=2.5):
+def check(S, T, E, K, dtype, scoring, bias=None, mask=None, logits=None, seed=0, scale=2.5, rel=REL, rel_grad=REL,
+          floor=0.0, floor_grad=1e-37):
     base, rng = make(S, T, E, dtype, seed)
     if logits is None:
         logits = base
@@ -178,15 +179,15 @@ def check(S, T, E, K, dtype, scoring, bias=None, mask=None, logits=None, seed=0,
     ep.ep_route_backward(cfg, x, r, torch.from_numpy(dw).cuda(), torch.from_numpy(dl).cuda(), out, token_mask=m)
     torch.cuda.synchronize()
     assert (r.topk_idx.cpu().numpy() == f["idx"]).all()
-    assert (np.abs(r.topk_weights.cpu().numpy() - f["w"]) <= REL * np.abs(f["w"])).all()
+    assert (np.abs(r.topk_weights.cpu().numpy() - f["w"]) <= rel * np.abs(f["w"]) + floor).all()
     assert (r.tokens_per_expert.cpu().numpy() == f["count"]).all()
     assert (r.tokens_valid.cpu().numpy() == f["valid"]).all()
-    assert (np.abs(r.balance_loss.cpu().numpy() - f["loss"]) <= REL * f["loss"]).all()
+    assert (np.abs(r.balance_loss.cpu().numpy() - f["loss"]) <= rel * f["loss"]).all()
     g, mag = plain_grad(f, scoring, scale, dw.astype(np.float64), dl.astype(np.float64))
     half = 2.0 ** -8 if dtype == "bf16" else 0.0
     got = out.float().cpu().numpy()
     err = np.abs(got - g)
-    within(err, REL * mag + half * np.abs(g) + 1e-37)
+    within(err, rel_grad * mag + half * np.abs(g) + floor_grad)
     # each gradient alone, and the forward without a balance loss
     r2 = ep.alloc_route(cfg)
     ep.ep_route(cfg, x, r2, bias=b, token_mask=m)
@@ -196,7 +197,7 @@ def check(S, T, E, K, dtype, scoring, bias=None, mask=None, logits=None, seed=0,
                              None if use_w else torch.from_numpy(dl).cuda(), out, token_mask=m)
         g, mag = plain_grad(f, scoring, scale, dw.astype(np.float64) * use_w, dl.astype(np.float64) * (not use_w))
         err = np.abs(out.float().cpu().numpy() - g)
-        within(err, REL * mag + half * np.abs(g) + 1e-37)
+        within(err, rel_grad * mag + half * np.abs(g) + floor_grad)
     return f, got
 
 
@@ -422,6 +423,39 @@ def test_many_tokens_masked_and_special(dtype, scoring):
     mask = (rng.uniform(size=(S, T)) < 0.5).astype(np.uint8)
     for b, m in ((None, None), (bias, None), (bias, mask)):
         f, got = check(S, T, E, K, dtype, scoring, b, m, logits=x, seed=14)
+        assert np.isfinite(got).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [600, 4200])
+def test_long_logits(T, dtype, scoring):
+    """Logits to some hundreds beside masked and special rows, with one and with several tokens per wave.
+
+    A score's error is (2 * max|l| + 16) u, which is 64 u at |l| <= 24; a term of the gradient has at most four factors
+    with that error (s, a score in a sum, s_k and 1 / D).  A score below the smallest normal value, 2^-126, may become
+    0.  The chosen scores' sum D is above 1/2 here, so that moves a weight by at most 2.5 * 2^-126 * 2 < 2^-123, and a
+    gradient, whose factors beside s are below 2.5 * 4.5 * 2 * 2 < 64, by at most 2^-120.
+    """
+    S, E, K = 2, 130, 6
+    x, rng = make(S, T, E, dtype, 13)
+    x[0, 0:T:7] = float("-inf")
+    x[0, 1:T:7] = low_of(dtype)
+    x[0, 2:T:7] = float("nan")
+    x[0, 3:T:7, 4:] = float("-inf")
+    x[0, 4:T:7, ::2] = float("nan")
+    x[1, 5:T:7, 7] = float("inf")
+    x[1, 6:T:7] *= 40.0
+    top = float(x[1, 6:T:7].abs().max())
+    assert 200 < top < 1000
+    rel = (2 * top + 16) * U
+    bias = np.linspace(-0.1, 0.1, E).astype(np.float32)
+    mask = (rng.uniform(size=(S, T)) < 0.5).astype(np.uint8)
+    for b, m in ((None, None), (bias, None), (bias, mask)):
+        f, got = check(S, T, E, K, dtype, scoring, b, m, logits=x, seed=14, rel=rel, rel_grad=4 * rel, floor=2.0 ** -123,
+                       floor_grad=2.0 ** -120)
+        assert (f["D"][1, 6::7][f["there"][1, 6::7].any(1)] > 0.5).all()
         assert np.isfinite(got).all()
 
 
