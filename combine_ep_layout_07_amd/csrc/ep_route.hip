@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads) k_route_rows(RouteArgs a) {
                 const float b = e0 + j < E ? a.bias[e0 + j] : 0.0f;
                 v = v > -INFINITY && b == b ? sc[j] + b : -INFINITY;
             }
-            const uint32_t u = __float_as_uint(v);
+            const uint32_t u = __float_as_uint(v + 0.0f);  // -0 is +0: they tie, and their bits would not
             const uint32_t up = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
             key[j] = v > -INFINITY ? (up & ~(uint32_t)kLow) | (uint32_t)(kLow - (e0 + j)) : 0u;
         }

@@ -474,3 +474,18 @@ def test_many_tokens_on_unaligned_rows():
         ep.ep_route_backward(cfg, flat[1:], a, dw, dl, ga[1:])
         ep.ep_route_backward(cfg, flat[1:].clone(), b, dw, dl, gb)
         assert torch.equal(ga[1:], gb[:-1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,E", [(33, 64), (2050, 64), (500, 300), (8200, 300)])
+def test_both_zeros_are_one_value(T, E, dtype, scoring):
+    """-0 and +0 tie, with one and with several tokens per wave: the lowest index is chosen, whichever zero it holds."""
+    rng = np.random.default_rng(T + E)
+    x = torch.from_numpy(rng.choice(np.float32([0.0, -0.0, -1.0, 1.0]), size=(1, T, E), p=(0.4, 0.4, 0.19, 0.01)))
+    x = x.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    check(1, T, E, 8, dtype, scoring, logits=x, seed=15)
+    x[:] = -1.0  # no other tie among the best
+    x[:, :, 2], x[:, :, 5] = -0.0, 0.0
+    check(1, T, E, 1, dtype, scoring, logits=x, seed=15)
