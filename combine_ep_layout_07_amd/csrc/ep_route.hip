@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(RouteArgs a) {
 // replaced by the expert (lowest first), so that keys differ and a round is a
 // maximum, a comparison and the owner's removal.  Where neighbours among the
 // K + 1 best agree in the bits that are left (with a bias: the last two do, or
-// two lie closer than their rounding tells apart), the choice is made again from
-// whole keys, in 64 bits with a bias.
+// two lie closer than their rounding tells apart, the K-th and the end of the next
+// bin included), the choice is made again from whole keys, in 64 bits with a bias.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_bits(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
@@ -657,7 +657,11 @@ __global__ void __launch_bounds__(kThreads) k_route_rows(RouteArgs a) {
         if (a.bias) {
             // s + bias in 32 bits is within 5e-7 * max(1, |s + bias|) of its
             // value (s to 3 * 2^-24, the sum's rounding 2^-24 relative).
-            const float mine = idx >= 0 ? sk + a.bias[idx] : -INFINITY;
+            // Past the K-th the order inside a bin is not known: the end of the
+            // (K+1)-th's bin bounds every key that was not chosen.
+            const uint32_t end = prev | (uint32_t)kLow;
+            float mine = idx >= 0 ? sk + a.bias[idx] : -INFINITY;
+            if (li == K && idx >= 0) mine = __uint_as_float(end ^ (end >> 31 ? 0x80000000u : 0xffffffffu));
             const float next = __int_as_float(shfl(__float_as_int(mine), lane + 1));
             const float unit = fmaxf(1.0f, fmaxf(fabsf(mine), fabsf(next)));
             again |= li < K && next > -INFINITY && !(mine - next > 1e-6f * unit);

@@ -489,3 +489,29 @@ def test_both_zeros_are_one_value(T, E, dtype, scoring):
     x[:] = -1.0  # no other tie among the best
     x[:, :, 2], x[:, :, 5] = -0.0, 0.0
     check(1, T, E, 1, dtype, scoring, logits=x, seed=15)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [1, 3])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 300])
+def test_many_tokens_with_near_ties_around_a_bins_end(E, scoring, K):
+    """Two experts of different scores and biases, whose keys lie within rounding of each other around 1.25, the end of
+    a bin of 256 and of 512 steps of 2^-23, one of them the K-th, and an expert of a lower index well below both in the
+    lower bin."""
+    T, step = 8200, 2.0 ** -23
+    rng = np.random.default_rng(E + K)
+    l = np.full(E, -3.0)
+    l[20:20 + K - 1] = 2.0  # clear winners
+    near = [5, 9, 12]
+    l[near] = 0.0, -0.7, 0.3
+    s = 1 / (1 + np.exp(-l)) if scoring == "sigmoid" else np.exp(l) / np.exp(l).sum()
+    bias = np.zeros(E, np.float32)
+    bias[near] = 1.25 - s[near]
+    bias[20:20 + K - 1] = 1.25
+    # The scores that make the keys, steps above 1.25 with the biases as rounded, and their logits.
+    want = 1.25 + np.stack([rng.uniform(lo, hi, T) for lo, hi in ((-200, -60), (-1, 1), (-1, 1))], 1) * step - bias[near]
+    rest = np.exp(np.delete(l, near)).sum() / (1 - want.sum(1, keepdims=True))
+    x = np.tile(l.astype(np.float32), (1, T, 1))
+    x[0][:, near] = np.log(want / (1 - want)) if scoring == "sigmoid" else np.log(want * rest)
+    check(1, T, E, K, "fp32", scoring, bias, logits=torch.from_numpy(x), seed=16)
