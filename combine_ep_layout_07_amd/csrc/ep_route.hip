@@ -70,6 +70,15 @@ __device__ __forceinline__ double sigmoid(double l) {
     return (l >= 0.0 ? 1.0 : z) / (1.0 + z);
 }
 
+// Keys s + bias in 32 bits that lie closer than this times max(1, |key|) are
+// compared in 64 bits.  The error of their difference, u = 2^-24: the softmax sum
+// is off by a step of u at each addition, 15 in a lane and 6 across the lanes, by
+// 4 u of its exponentials, the division by u; that scales both scores and moves
+// their difference, at most 1, by 26 u.  Each score has 5 u more of its own (the
+// two are at most 1 together) and each sum with the bias rounds once: 33 u, and 3
+// for the difference and its bound.  (A sigmoid score is off by 3 u.)
+constexpr float kKeyError = 36.0f * 0x1p-24f;
+
 // K rounds of "largest key, lowest index".  Lane k of the result holds the k-th
 // expert and its logit, bit j of `taken` says that the lane's j-th expert was
 // chosen, `close` that two of the K+1 best keys lie closer than rounding tells
@@ -100,11 +109,9 @@ __device__ __forceinline__ int select(Key (&key)[PER], const float (&l)[PER], in
         const Key top = wave_max(best);
         if (!(top > (Key)-INFINITY)) break;
         if (want_gap && k > 0) {
-            // A key s + bias in 32 bits is within 5e-7 * max(1, |key|) of its
-            // value (s to 3 * 2^-24, the sum's rounding 2^-24 relative).
             const Key a = top < 0 ? -top : top, b = prev < 0 ? -prev : prev;
             const Key unit = a > b ? (a > 1 ? a : (Key)1) : (b > 1 ? b : (Key)1);
-            if (!(prev - top > (Key)1e-6 * unit)) close = true;
+            if (!(prev - top > (Key)kKeyError * unit)) close = true;
         }
         prev = top;
         if (k == K) break;
@@ -655,8 +662,6 @@ __global__ void __launch_bounds__(kThreads) k_route_rows(RouteArgs a) {
         float lk = idx >= 0 ? take<T>(row[idx], lowest(row), true) : 0.0f;
         float sk = idx < 0 ? 0.0f : (SIG ? fast_sigmoid(lk) : exp_below(lk, top) * by);
         if (a.bias) {
-            // s + bias in 32 bits is within 5e-7 * max(1, |s + bias|) of its
-            // value (s to 3 * 2^-24, the sum's rounding 2^-24 relative).
             // Past the K-th the order inside a bin is not known: the end of the
             // (K+1)-th's bin bounds every key that was not chosen.
             const uint32_t end = prev | (uint32_t)kLow;
@@ -664,7 +669,7 @@ __global__ void __launch_bounds__(kThreads) k_route_rows(RouteArgs a) {
             if (li == K && idx >= 0) mine = __uint_as_float(end ^ (end >> 31 ? 0x80000000u : 0xffffffffu));
             const float next = __int_as_float(shfl(__float_as_int(mine), lane + 1));
             const float unit = fmaxf(1.0f, fmaxf(fabsf(mine), fabsf(next)));
-            again |= li < K && next > -INFINITY && !(mine - next > 1e-6f * unit);
+            again |= li < K && next > -INFINITY && !(mine - next > kKeyError * unit);
         }
         // bf16 logits lie in the bits that are left: equal ones are equal.
         if (sizeof(T) == 2 && !a.bias) again = false;

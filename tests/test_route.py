@@ -515,3 +515,23 @@ def test_many_tokens_with_near_ties_around_a_bins_end(E, scoring, K):
     x = np.tile(l.astype(np.float32), (1, T, 1))
     x[0][:, near] = np.log(want / (1 - want)) if scoring == "sigmoid" else np.log(want * rest)
     check(1, T, E, K, "fp32", scoring, bias, logits=torch.from_numpy(x), seed=16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,K", [(5, 1024, 1), (8200, 256, 2)])
+def test_choice_where_the_softmax_sum_rounds_one_way(T, E, K):
+    """The softmax sum 1 + n t, t just below half a step of 1, rounds to 1 in 32 bits when every addition meets one more
+    t, n of them being as many as the additions after the lane that holds the 1.  The expert with bias 1 - n 2^-24 and
+    score t is the better one by 2^-24, and behind by (n - 1) 2^-24 in 32 bits."""
+    x = torch.full((1, T, E), float("-inf"))
+    if E == 1024:  # 16 experts a lane, summed by a scan towards the last lane
+        best, other, small = 1008, 0, list(range(1009, 1024)) + [16 * l for l in (62, 61, 59, 55, 47, 0)]
+    else:          # 16 experts a lane of 16 lanes, folded by halves
+        best, other, small = 0, 16, list(range(1, 16)) + [16 * l for l in (8, 4, 2, 1)]
+    x[0, :, small] = float(np.log(U * (1 - 2.0 ** -9)))
+    x[0, :, best] = 0.0
+    bias = np.zeros(E, np.float32)
+    bias[other] = 1 - len(small) * U
+    f = plain(x.numpy(), K, "softmax", 1.0, bias, None, low_of("fp32"))
+    assert (f["idx"][0, :, 0] == other).all()
+    check(1, T, E, K, "fp32", "softmax", bias, logits=x, seed=17)
