@@ -524,3 +524,34 @@ def test_no_rows():
     ep.ep_expert_mm(cfg, b, z, w, o)
     ep.ep_expert_mm_backward(cfg, b, z, w, o, ep.alloc_expert_backward(cfg), pre=o, d_x=z, d_w=dw, d_bias=db)
     assert (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.gpu
+def test_gelu_in_its_tail():
+    """v Phi(v) and its slope to a few u of their own size, down to where Phi leaves the normal numbers.
+
+    exp(-v^2 / 2) has the roundings of v^2, of its product with a constant and of that constant, each u of an exponent
+    v^2 / 2: 1.5 v^2 u; everything else (the tail's polynomial, the reciprocal, exp2, a few products) is below 24 u."""
+    v = torch.linspace(-13.0, 13.0, 417).bfloat16()
+    n = len(v)
+    x = torch.zeros((n, 8)).bfloat16()
+    x[:, 0] = v
+    w = torch.zeros((1, 8, 8)).bfloat16()
+    w[:, :, 0] = 1.0
+    v64 = v.double()
+    tol = (1.5 * v64 * v64 + 24) * U
+    cfg = ep.make_expert_config(1, n, 8, 8, activation="gelu")
+    out = torch.empty((n, 8), dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_mm(cfg, torch.tensor([0, n], dtype=torch.int32).cuda(), x.cuda(), w.cuda(), out)
+    want = v64 * phi(v64)
+    assert ((out.cpu().double()[:, 0] - want).abs() <= (H + tol * (1 + H)) * want.abs()).all()
+    # one row per expert: d_bias is the slope itself
+    cfg = ep.make_expert_config(n, n, 8, 8, activation="gelu")
+    base = torch.arange(n + 1, dtype=torch.int32).cuda()
+    pre, one = v[:, None].expand(n, 8).contiguous().cuda(), torch.ones((n, 8), dtype=torch.bfloat16, device="cuda")
+    db = torch.empty((n, 8), device="cuda")
+    ep.ep_expert_mm_backward(cfg, base, None, torch.zeros((n, 8, 8), dtype=torch.bfloat16, device="cuda"), one,
+                             ep.alloc_expert_backward(cfg), pre=pre, d_bias=db)
+    bell = v64 * torch.exp(-0.5 * v64 * v64) / np.sqrt(2 * np.pi)
+    want, mag = phi(v64) + bell, phi(v64) + bell.abs()
+    assert ((db.cpu().double()[:, 0] - want).abs() <= tol * mag).all()
