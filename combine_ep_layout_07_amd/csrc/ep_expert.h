@@ -90,9 +90,11 @@ __device__ __forceinline__ Segment find_tile(const int32_t *base, int E, int64_t
 
 // 1 / (1 + exp(-v)) without overflow on either side, from the hardware's exp2
 // and reciprocal: off by a few 2^-24 of 1 (the library's expf and division took
-// half of the time of an epilogue).
+// half of the time of an epilogue).  exp2 returns nothing below the normal
+// numbers, so exp(-|v|) is the square of half the exponent's: v times it is
+// normal down to -91.
 __device__ __forceinline__ float logistic(float v) {
-    const float z = __builtin_amdgcn_exp2f(fabsf(v) * -1.44269504f);
+    const float y = __builtin_amdgcn_exp2f(fabsf(v) * -0.72134752f), z = y * y;
     return (v >= 0.0f ? 1.0f : z) * __builtin_amdgcn_rcpf(1.0f + z);
 }
 

@@ -555,3 +555,25 @@ def test_gelu_in_its_tail():
     bell = v64 * torch.exp(-0.5 * v64 * v64) / np.sqrt(2 * np.pi)
     want, mag = phi(v64) + bell, phi(v64) + bell.abs()
     assert ((db.cpu().double()[:, 0] - want).abs() <= tol * mag).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "swiglu"])
+def test_silu_in_its_tail(act):
+    """v / (1 + exp(-v)) where exp(v) is below the normal numbers but the product is not, or hardly.  exp(v) has the
+    roundings of an exponent |v| (2 |v| u) and two of half a step of 2^-149, which v multiplies."""
+    v = torch.arange(-91.5, -80.0, 0.5).bfloat16()
+    n = len(v)
+    x = torch.zeros((n, 8)).bfloat16()
+    x[:, 0], x[:, 1] = v, 1.0
+    w = torch.zeros((1, cols_of(8, act), 8)).bfloat16()
+    w[:, :8, 0] = 1.0
+    w[:, 8:, 1] = 1.0
+    cfg = ep.make_expert_config(1, n, 8, 8, activation=act)
+    out = torch.empty((n, 8), dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_mm(cfg, torch.tensor([0, n], dtype=torch.int32).cuda(), x.cuda(), w.cuda(), out)
+    v64 = v.double()
+    want = v64 * torch.exp(v64)
+    assert (want.abs() >= 2.0 ** -126).all()
+    tol = (H + (2 * v64.abs() + 16) * U * (1 + H)) * want.abs() + v64.abs() * 2.0 ** -149 * (1 + H)
+    assert ((out.cpu().double()[:, 0] - want).abs() <= tol).all()
