@@ -172,10 +172,10 @@ __global__ void __launch_bounds__(kWave *W) k_route(RouteArgs a) {
     constexpr int kWaves = W, kThreads = kWaves * kWave;
     const int lane = lane_id(), wave = threadIdx.x / kWave;
     const int s = blockIdx.y, E = a.E, K = a.K;
-    float psum[PER];
+    double psum[PER];  // equal probabilities round one way: 1024 additions in fp32 were off by 1.5e-5
     int cnt[PER], seen = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) psum[j] = 0.0f, cnt[j] = 0;
+    for (int j = 0; j < PER; ++j) psum[j] = 0.0, cnt[j] = 0;
     if (BAL && blockIdx.x == 0 && threadIdx.x == 0) a.part_done[s] = 0;  // for k_route_sum
     for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.T; t += (int64_t)gridDim.x * kWaves) {
         const int64_t g = (int64_t)s * a.T + t;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kWave *W) k_route(RouteArgs a) {
             const float r = SIG ? 1.0f / (all + 1e-20f) : 1.0f;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                psum[j] += any ? sc[j] * r : 0.0f;
+                psum[j] += (double)(any ? sc[j] * r : 0.0f);
                 cnt[j] += (taken >> j) & 1u;
             }
         }
@@ -250,18 +250,18 @@ __global__ void __launch_bounds__(kWave *W) k_route(RouteArgs a) {
         __shared__ int ls[kWaves];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            lp[wave][lane * PER + j] = psum[j];
+            lp[wave][lane * PER + j] = (float)psum[j];
             lc[wave][lane * PER + j] = cnt[j];
         }
         if (lane == 0) ls[wave] = seen;
         __syncthreads();
         const int64_t unit = (int64_t)s * gridDim.x + blockIdx.x;
         for (int e = threadIdx.x; e < a.pitch; e += kThreads) {
-            float p = 0.0f;
+            double p = 0.0;
             int c = 0;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) p += lp[w][e], c += lc[w][e];
-            a.part_p[unit * a.pitch + e] = p;
+            for (int w = 0; w < kWaves; ++w) p += (double)lp[w][e], c += lc[w][e];
+            a.part_p[unit * a.pitch + e] = (float)p;
             a.part_cnt[unit * a.pitch + e] = c;
         }
         if (threadIdx.x == 0) {
@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kWave *W) k_route(RouteArgs a) {
 // partial sum of four neighbouring experts in order, eight loads in flight (one
 // at a time took 74 us instead of 6 at 1024 partial sums of 256 experts).  The
 // last workgroup to finish adds the shares of the loss, in order.  Sums over
-// tokens and experts are held in 64 bits.
+// tokens and experts are held in 64 bits; a wave's and a workgroup's sums are
+// rounded to 32 once each.
 constexpr int kSumThreads = 256, kSumExperts = 32, kSumQuads = kSumExperts / 4, kSumParts = kSumThreads / kSumQuads;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -605,11 +606,11 @@ __global__ void __launch_bounds__(kThreads) k_route_rows(RouteArgs a) {
     __shared__ int ls[kWaves];
     const int lane = lane_id(), wave = threadIdx.x / kWave, li = lane % L, e0 = li * PER;
     const int s = blockIdx.y, E = a.E, K = a.K;
-    float psum[PER];
+    double psum[PER];  // as in k_route
     int seen = 0;
     if (BAL) {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) psum[j] = 0.0f;
+        for (int j = 0; j < PER; ++j) psum[j] = 0.0;
         for (int e = threadIdx.x; e < kAll; e += kThreads) hist[e] = 0;
         if (blockIdx.x == 0 && threadIdx.x == 0) a.part_done[s] = 0;  // for k_route_sum
         __syncthreads();
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(kThreads) k_route_rows(RouteArgs a) {
             seen += any && li == 0;
             const float r = !any ? 0.0f : (SIG ? 1.0f / (all + 1e-20f) : 1.0f);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) psum[j] += sc[j] * r;
+            for (int j = 0; j < PER; ++j) psum[j] += (double)(sc[j] * r);
         }
     }
     if (BAL) {
@@ -717,22 +718,23 @@ __global__ void __launch_bounds__(kThreads) k_route_rows(RouteArgs a) {
 #pragma unroll
         for (int d = L; d < kWave; d <<= 1) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) psum[j] += __int_as_float(shfl(__float_as_int(psum[j]), lane ^ d));
+            for (int j = 0; j < PER; ++j)
+                psum[j] += __hiloint2double(shfl(__double2hiint(psum[j]), lane ^ d), shfl(__double2loint(psum[j]), lane ^ d));
         }
 #pragma unroll
         for (int d = 32; d; d >>= 1) seen += shfl(seen, lane ^ d);
         if (lane < L) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) lp[wave][e0 + j] = psum[j];
+            for (int j = 0; j < PER; ++j) lp[wave][e0 + j] = (float)psum[j];
         }
         if (lane == 0) ls[wave] = seen;
         __syncthreads();
         const int64_t unit = (int64_t)s * gridDim.x + blockIdx.x;
         for (int e = threadIdx.x; e < a.pitch; e += kThreads) {
-            float p = 0.0f;
+            double p = 0.0;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) p += lp[w][e];
-            a.part_p[unit * a.pitch + e] = p;
+            for (int w = 0; w < kWaves; ++w) p += (double)lp[w][e];
+            a.part_p[unit * a.pitch + e] = (float)p;
             a.part_cnt[unit * a.pitch + e] = hist[e];
         }
         if (threadIdx.x == 0) a.part_seen[unit] = ls[0] + ls[1] + ls[2] + ls[3];

@@ -535,3 +535,16 @@ def test_choice_where_the_softmax_sum_rounds_one_way(T, E, K):
     f = plain(x.numpy(), K, "softmax", 1.0, bias, None, low_of("fp32"))
     assert (f["idx"][0, :, 0] == other).all()
     check(1, T, E, K, "fp32", "softmax", bias, logits=x, seed=17)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("S,T,E", [(256, 65536, 13), (128, 16384, 595)])
+def test_balance_loss_of_long_sources(S, T, E, scoring):
+    """Equal logits: every p is 1 / E and rounds the same way, so that a chain of 32-bit additions drifts.  All tokens
+    choose expert 0, f_0 = E, and the loss is 1."""
+    cfg = ep.make_route_config(S, T, E, 1, "bf16", scoring)
+    r = ep.alloc_route(cfg, balance=True)
+    ep.ep_route(cfg, torch.zeros((S, T, E), dtype=torch.bfloat16, device="cuda"), r)
+    assert (r.topk_idx == 0).all() and (r.tokens_per_expert[:, 0] == T).all()
+    assert ((r.balance_loss.double() - 1).abs() <= REL).all()
