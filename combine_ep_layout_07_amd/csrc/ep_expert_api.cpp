@@ -107,7 +107,8 @@ int ep_expert_mm_backward(const ep_expert_config_t *cfg, const int32_t *expert_b
     const int rc = make_args(cfg, expert_base_dev, x_dev, w_dev, &a);
     if (rc != EP_OK) return rc;
     if (a.fp8) return EP_ERR_UNSUPPORTED;
-    if ((!d_x_dev && !d_w_dev && !d_bias_dev) || !aligned(d_x_dev, 16) || !aligned(d_w_dev, 16) ||
+    // Without rows a caller's d_x is empty and may have no address.
+    if ((a.rows > 0 && !d_x_dev && !d_w_dev && !d_bias_dev) || !aligned(d_x_dev, 16) || !aligned(d_w_dev, 16) ||
         !aligned(d_bias_dev, 4) || !aligned(pre_dev, 16) || !aligned(d_out_dev, 16) || !scratch_dev ||
         !aligned(scratch_dev, 16))
         return EP_ERR_INVALID_ARG;

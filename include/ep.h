@@ -466,7 +466,8 @@ int ep_expert_mm(const ep_expert_config_t *cfg, const int32_t *expert_base_dev, 
  *   d = act'(pre) d_out,  d_x[r] = d[r] W_e  (bf16 [num_rows][I]),
  *   d_w[e] = sum over the expert's rows of d[r]^T x[r]  (bf16 [E][Nw][I]),
  *   d_bias[e] = sum of d[r]  (fp32 [E][Nw]);
- * an expert without rows gets zeros.  Each gradient may be NULL (not all).
+ * an expert without rows gets zeros.  Each gradient may be NULL (not all, unless
+ * num_rows is 0).
  * pre_dev is not needed without an activation, x_dev only for d_w.  The
  * matrix units take d rounded to bf16; d_bias sums the unrounded values, in a
  * fixed order.  Padding rows count like others: ep_combine_backward writes

@@ -577,3 +577,21 @@ def test_silu_in_its_tail(act):
     assert (want.abs() >= 2.0 ** -126).all()
     tol = (H + (2 * v64.abs() + 16) * U * (1 + H)) * want.abs() + v64.abs() * 2.0 ** -149 * (1 + H)
     assert ((out.cpu().double()[:, 0] - want).abs() <= tol).all()
+
+
+@pytest.mark.gpu
+def test_no_rows_and_their_gradient_alone():
+    cfg = ep.make_expert_config(2, 0, 64, 32, activation="gelu")
+    z = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((2, 32, 64), dtype=torch.bfloat16, device="cuda")
+    o = torch.zeros((0, 32), dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ep.ep_expert_mm_backward(cfg, b, None, w, o, ep.alloc_expert_backward(cfg), pre=o, d_x=z)
+
+
+def test_no_gradient_wanted():
+    """Refused with rows; without any, an empty d_x has no address, and there is nothing to do."""
+    f = 0x10000
+    for rows, code in ((10, BAD), (0, ep.EP_OK)):
+        cfg = ep.make_expert_config(2, rows, 64, 32)
+        assert ep._lib.ep_expert_mm_backward(ctypes.byref(cfg), f, f, f, None, f, None, None, None, f, None) == code
