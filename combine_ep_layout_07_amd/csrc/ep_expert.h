@@ -58,11 +58,14 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
-// All tiles of `size` rows of the first E experts' segments.
+// All tiles of `size` rows of the first E experts' segments.  A table that
+// decreases can count every row hundreds of times; a grid holds 2^24 workgroups,
+// so the lanes' bound changes no count that a launch uses and keeps the sum
+// positive.
 __device__ __forceinline__ int count_tiles(const int32_t *base, int E, int64_t rows, int size) {
     int n = 0;
     for (int e = lane_id(); e < E; e += kWave) n += (segment_of(base, e, rows).n + size - 1) / size;
-    return read_lane(wave_scan(n), kWave - 1);
+    return read_lane(wave_scan(min(n, (1 << 25) - 1)), kWave - 1);
 }
 
 // Tile `tile` of `size` rows, counted over the experts in order: a scan over

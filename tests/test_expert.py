@@ -595,3 +595,19 @@ def test_no_gradient_wanted():
     for rows, code in ((10, BAD), (0, ep.EP_OK)):
         cfg = ep.make_expert_config(2, rows, 64, 32)
         assert ep._lib.ep_expert_mm_backward(ctypes.byref(cfg), f, f, f, None, f, None, None, None, f, None) == code
+
+
+@pytest.mark.gpu
+def test_table_that_decreases_stays_inside():
+    """Every second of 1024 experts claims all of 80 million rows: their tiles together pass 2^31, and the sums of the
+    experts past the partial sums that there are read nothing."""
+    E, rows, N = 1024, 80_000_000, 8
+    cfg = ep.make_expert_config(E, rows, 8, N)
+    base = torch.tensor([0, rows] * (E // 2) + [0], dtype=torch.int32).cuda()
+    d_out = torch.zeros((rows, N), dtype=torch.bfloat16, device="cuda")
+    d_out[rows - 1] = 1.0
+    db = torch.full((E, N), 7.0, device="cuda")
+    w = torch.zeros((E, N, 8), dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_mm_backward(cfg, base, None, w, d_out, ep.alloc_expert_backward(cfg), d_bias=db)
+    torch.cuda.synchronize()
+    assert (db[0] == 1).all() and (db[1:] == 0).all()
