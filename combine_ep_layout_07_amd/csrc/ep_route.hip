@@ -60,6 +60,22 @@ __device__ __forceinline__ void load_logits(const T *row, int E, int lane, bool 
     }
 }
 
+// exp(d + e), d <= 0, e far below d, from the hardware's exp2: the argument's
+// product with log2(e) is carried in two parts, so the error is a few 2^-24 of
+// the value however long the argument is (with one part: |d| 2^-24).
+__device__ __forceinline__ float exp_of(float d, float e) {
+    const float p = d * 1.44269502f;
+    const float r = fmaf(e, 1.44269502f, fmaf(d, 1.92596303e-8f, fmaf(d, 1.44269502f, -p)));
+    return __builtin_amdgcn_exp2f(p) * fmaf(r, 0.69314718f, 1.0f);
+}
+// exp(l - top), l <= top, with the difference's own rounding; 0 where it is
+// below the normal numbers (and for -inf).
+__device__ __forceinline__ float exp_below(float l, float top) {
+    const float d = l - top, z = d - l, e = (l - (d - z)) - (top + z);
+    const float v = exp_of(d, e);
+    return d > -110.0f ? v : 0.0f;
+}
+
 // 1 / (1 + exp(-l)) without overflow on either side; 0 for -inf.
 __device__ __forceinline__ float sigmoid(float l) {
     const float z = expf(-fabsf(l));
@@ -147,7 +163,7 @@ __device__ __forceinline__ float sum_of(const float (&v)[PER]) {
 template <int PER, bool SIG>
 __device__ __forceinline__ void scores(const float (&l)[PER], float top, float (&s)[PER], float &inv, float &all) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) s[j] = SIG ? sigmoid(l[j]) : expf(l[j] - top);
+    for (int j = 0; j < PER; ++j) s[j] = SIG ? sigmoid(l[j]) : exp_below(l[j], top);
     all = sum_of(s);
     inv = 1.0f;
     if (!SIG) {
@@ -227,7 +243,7 @@ __global__ void __launch_bounds__(kWave *W) k_route(RouteArgs a) {
             }
         }
         const bool chosen = lane < n;
-        const float sk = chosen ? (SIG ? sigmoid(lsel) : expf(lsel - top) * inv) : 0.0f;
+        const float sk = chosen ? (SIG ? sigmoid(lsel) : exp_below(lsel, top) * inv) : 0.0f;
         const float D = wave_sum(sk) + 1e-20f;
         if (lane < K) {
             a.topk_idx[g * K + lane] = idx;
@@ -513,21 +529,6 @@ __device__ __forceinline__ double group_sum(double v) {
     return v;
 }
 
-// exp(d + e), d <= 0, e far below d, from the hardware's exp2: the argument's
-// product with log2(e) is carried in two parts, so the error is a few 2^-24 of
-// the value however long the argument is (with one part: |d| 2^-24).
-__device__ __forceinline__ float exp_of(float d, float e) {
-    const float p = d * 1.44269502f;
-    const float r = fmaf(e, 1.44269502f, fmaf(d, 1.92596303e-8f, fmaf(d, 1.44269502f, -p)));
-    return __builtin_amdgcn_exp2f(p) * fmaf(r, 0.69314718f, 1.0f);
-}
-// exp(l - top), l <= top, with the difference's own rounding; 0 where it is
-// below every fp32 (and for -inf).
-__device__ __forceinline__ float exp_below(float l, float top) {
-    const float d = l - top, z = d - l, e = (l - (d - z)) - (top + z);
-    const float v = exp_of(d, e);
-    return d > -110.0f ? v : 0.0f;
-}
 __device__ __forceinline__ float fast_sigmoid(float l) {
     const float m = fabsf(l), v = exp_of(-m, 0.0f), z = m < 110.0f ? v : 0.0f;
     return (l >= 0.0f ? 1.0f : z) * __builtin_amdgcn_rcpf(1.0f + z);

@@ -548,3 +548,25 @@ def test_balance_loss_of_long_sources(S, T, E, scoring):
     ep.ep_route(cfg, torch.zeros((S, T, E), dtype=torch.bfloat16, device="cuda"), r)
     assert (r.topk_idx == 0).all() and (r.tokens_per_expert[:, 0] == T).all()
     assert ((r.balance_loss.double() - 1).abs() <= REL).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [600, 8200])
+def test_weights_of_long_logits_to_their_last_bits(T, scoring):
+    """One logit near 80 beside others near 0: l - max loses bits of l in 32 bits.  A score's error does not grow with the
+    logits: exp to 4 u, the division and the product with it 2 u, the sum over K of them K u more, the scale u."""
+    S, E, K = 1, 200, 6
+    rng = np.random.default_rng(T)
+    x = rng.uniform(-1, 1, size=(S, T, E)).astype(np.float32)
+    if scoring == "sigmoid":
+        x -= 40.0
+    top = rng.integers(0, E, size=T)
+    x[0, np.arange(T), top] += np.float32(80.0)
+    f = plain(x, K, scoring, 2.5, None, None, low_of("fp32"))
+    cfg = ep.make_route_config(S, T, E, K, "fp32", scoring, 2.5)
+    r = ep.alloc_route(cfg)
+    ep.ep_route(cfg, torch.from_numpy(x).cuda(), r)
+    w = r.topk_weights.cpu().numpy()
+    assert (r.topk_idx.cpu().numpy() == f["idx"]).all()
+    within(np.abs(w - f["w"]), 24 * U * f["w"])
