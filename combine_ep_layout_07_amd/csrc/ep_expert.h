@@ -144,6 +144,8 @@ __device__ __forceinline__ float activate_slope(int act, float v) {
     return 1.0f;
 }
 
+// Rows of the tiles that the products take (0: no such product).
+void expert_tiles(const ExpertArgs &a, int *forward, int *d_x, int *d_w);
 hipError_t launch_expert(const ExpertArgs &a, hipStream_t st);
 hipError_t launch_expert_backward(const ExpertArgs &a, hipStream_t st);
 

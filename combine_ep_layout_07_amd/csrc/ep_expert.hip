@@ -912,31 +912,32 @@ double cost_32(const ExpertArgs &a) {
     return FP8 ? cost<MODE, FP8>(a, 32, 64, 512, 3, 0.65, 0.7) : cost<MODE, FP8>(a, 32, 64, 512, 3, 0.2, 0.32);
 }
 
-// The product in the cheapest tiles below 256 x 256, and its cost.
+// Rows of the cheapest tiles: 32, 64, 128 or 256 (d_w: 128 or 256).
 template <int MODE, bool FP8>
-double cost_small(const ExpertArgs &a) {
+int tile_rows(const ExpertArgs &a) {
     double c = cost_128<MODE, FP8>(a);
-    if (MODE == kDw) return c;
-    const double c64 = cost_64<MODE, FP8>(a), c32 = cost_32<MODE, FP8>(a);
-    c = c64 < c ? c64 : c;
-    return c32 < c ? c32 : c;
+    int rows = 128;
+    if (MODE != kDw) {
+        const double c64 = cost_64<MODE, FP8>(a), c32 = cost_32<MODE, FP8>(a);
+        if (c64 <= c) c = c64, rows = 64;
+        if (c32 <= c) c = c32, rows = 32;
+    }
+    return cost_wide<MODE, FP8>(a) < c ? 256 : rows;
 }
 template <int MODE, bool FP8>
-hipError_t run_small(const ExpertArgs &a, hipStream_t st) {
+hipError_t run_small(const ExpertArgs &a, int rows, hipStream_t st) {
     constexpr bool F = MODE == kForward;
     if constexpr (MODE != kDw) {
-        const double c = cost_small<MODE, FP8>(a);
-        if (c == cost_32<MODE, FP8>(a))
-            return run_tile<MODE, FP8, 32, F ? 64 : 128, F ? 2 : 1, F ? 2 : 4, 128, F ? 6 : 4>(a, st);
-        if (c == cost_64<MODE, FP8>(a)) return run_tile<MODE, FP8, 64, 128, 2, 2, 128, 3>(a, st);
+        if (rows == 32) return run_tile<MODE, FP8, 32, F ? 64 : 128, F ? 2 : 1, F ? 2 : 4, 128, F ? 6 : 4>(a, st);
+        if (rows == 64) return run_tile<MODE, FP8, 64, 128, 2, 2, 128, 3>(a, st);
     }
     return run_tile<MODE, FP8, 128, 128, 2, 2, 128, 2>(a, st);
 }
 
 template <bool FP8>
 hipError_t run_forward(const ExpertArgs &a, hipStream_t st) {
-    if (cost_wide<kForward, FP8>(a) < cost_small<kForward, FP8>(a)) return run_wide<FP8>(a, st);
-    return run_small<kForward, FP8>(a, st);
+    const int rows = tile_rows<kForward, FP8>(a);
+    return rows == 256 ? run_wide<FP8>(a, st) : run_small<kForward, FP8>(a, rows, st);
 }
 
 // Both gradients go in one launch where both are best in wide tiles (565 us in
@@ -944,16 +945,22 @@ hipError_t run_forward(const ExpertArgs &a, hipStream_t st) {
 // 82 in one).
 hipError_t run_back(const ExpertArgs &a, hipStream_t st) {
     const bool x = a.d_x && a.rows > 0, w = a.d_w;
-    const bool wide_x = x && cost_wide<kDx, false>(a) < cost_small<kDx, false>(a);
-    const bool wide_w = w && cost_wide<kDw, false>(a) < cost_small<kDw, false>(a);
+    const int rows_x = tile_rows<kDx, false>(a), rows_w = tile_rows<kDw, false>(a);
+    const bool wide_x = x && rows_x == 256, wide_w = w && rows_w == 256;
     hipError_t rc = hipSuccess;
     if (wide_x || wide_w) rc = run_wide_back(a, wide_x, wide_w, st);
-    if (rc == hipSuccess && x && !wide_x) rc = run_small<kDx, false>(a, st);
-    if (rc == hipSuccess && w && !wide_w) rc = run_small<kDw, false>(a, st);
+    if (rc == hipSuccess && x && !wide_x) rc = run_small<kDx, false>(a, rows_x, st);
+    if (rc == hipSuccess && w && !wide_w) rc = run_small<kDw, false>(a, rows_w, st);
     return rc;
 }
 
 }  // namespace
+
+void expert_tiles(const ExpertArgs &a, int *forward, int *d_x, int *d_w) {
+    *forward = a.fp8 ? tile_rows<kForward, true>(a) : tile_rows<kForward, false>(a);
+    *d_x = a.fp8 ? 0 : tile_rows<kDx, false>(a);
+    *d_w = a.fp8 ? 0 : tile_rows<kDw, false>(a);
+}
 
 hipError_t launch_expert(const ExpertArgs &a, hipStream_t st) {
     if (a.rows == 0) return hipSuccess;

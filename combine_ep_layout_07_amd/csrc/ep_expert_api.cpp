@@ -37,10 +37,7 @@ uint64_t grad_bytes(const ep_expert_config_t *c) {
     return up256((uint64_t)c->num_rows * wide(c) * 2);
 }
 
-int make_args(const ep_expert_config_t *c, const int32_t *base, const void *x, const void *w, ep::ExpertArgs *out) {
-    const int rc = check_config(c);
-    if (rc != EP_OK) return rc;
-    if (!base || !aligned(base, 4) || !w || !aligned(w, 16) || !aligned(x, 16)) return EP_ERR_INVALID_ARG;
+void set_shape(const ep_expert_config_t *c, ep::ExpertArgs *out) {
     ep::ExpertArgs &a = *out;
     memset(&a, 0, sizeof(a));
     a.E = c->num_experts;
@@ -50,9 +47,16 @@ int make_args(const ep_expert_config_t *c, const int32_t *base, const void *x, c
     a.act = c->activation;
     a.fp8 = c->x_dtype == EP_DTYPE_FP8_E4M3FN;
     a.rows = c->num_rows;
-    a.base = base;
-    a.x = x;
-    a.w = w;
+}
+
+int make_args(const ep_expert_config_t *c, const int32_t *base, const void *x, const void *w, ep::ExpertArgs *out) {
+    const int rc = check_config(c);
+    if (rc != EP_OK) return rc;
+    if (!base || !aligned(base, 4) || !w || !aligned(w, 16) || !aligned(x, 16)) return EP_ERR_INVALID_ARG;
+    set_shape(c, out);
+    out->base = base;
+    out->x = x;
+    out->w = w;
     return EP_OK;
 }
 
@@ -76,6 +80,18 @@ int ep_query_expert_sizes(const ep_expert_config_t *cfg, ep_expert_sizes_t *sz) 
     sz->out = rows * cfg->out_features * 2;
     sz->pre = rows * Nw * 2;
     if (!fp8) sz->backward_scratch = grad_bytes(cfg) + ep::expert_row_tiles(rows, (int)E, ep::kActRows) * Nw * 4;
+    return EP_OK;
+}
+
+int ep_query_expert_tiles(const ep_expert_config_t *cfg, ep_expert_tiles_t *tiles) {
+    const int rc = check_config(cfg);
+    if (rc != EP_OK) return rc;
+    if (!tiles) return EP_ERR_INVALID_ARG;
+    memset(tiles, 0, sizeof(*tiles));
+    if (cfg->num_rows == 0) return EP_OK;
+    ep::ExpertArgs a;
+    set_shape(cfg, &a);
+    ep::expert_tiles(a, &tiles->forward, &tiles->d_x, &tiles->d_w);
     return EP_OK;
 }
 

@@ -93,6 +93,10 @@ class EpExpertSizes(ctypes.Structure):
         "x", "x_sf", "w", "w_sf", "bias", "out", "pre", "backward_scratch")]
 
 
+class EpExpertTiles(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("forward", "d_x", "d_w")]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
@@ -112,11 +116,12 @@ def _load():
     lib.ep_route.argtypes = [ctypes.POINTER(EpRouteConfig), P, P, P, ctypes.POINTER(EpRouteT), P]
     lib.ep_route_backward.argtypes = [ctypes.POINTER(EpRouteConfig), P, P, ctypes.POINTER(EpRouteT), P, P, P, P]
     lib.ep_query_expert_sizes.argtypes = [ctypes.POINTER(EpExpertConfig), ctypes.POINTER(EpExpertSizes)]
+    lib.ep_query_expert_tiles.argtypes = [ctypes.POINTER(EpExpertConfig), ctypes.POINTER(EpExpertTiles)]
     lib.ep_expert_mm.argtypes = [ctypes.POINTER(EpExpertConfig)] + [P] * 10
     lib.ep_expert_mm_backward.argtypes = [ctypes.POINTER(EpExpertConfig)] + [P] * 10
     for f in ("ep_query_sizes", "ep_layout", "ep_layout_no_alloc", "ep_dispatch", "ep_layout_dispatch", "ep_combine",
               "ep_combine_bias", "ep_combine_backward", "ep_query_route_sizes", "ep_route", "ep_route_backward",
-              "ep_query_expert_sizes", "ep_expert_mm", "ep_expert_mm_backward", "ep_version"):
+              "ep_query_expert_sizes", "ep_query_expert_tiles", "ep_expert_mm", "ep_expert_mm_backward", "ep_version"):
         getattr(lib, f).restype = ctypes.c_int
     lib.ep_status_string.argtypes = [ctypes.c_int]
     lib.ep_status_string.restype = ctypes.c_char_p
@@ -491,6 +496,14 @@ def ep_query_expert_sizes(cfg: EpExpertConfig) -> EpExpertSizes:
     if rc != EP_OK:
         raise EpError(rc, "ep_query_expert_sizes")
     return sz
+
+
+def ep_query_expert_tiles(cfg: EpExpertConfig) -> EpExpertTiles:
+    tiles = EpExpertTiles()
+    rc = _lib.ep_query_expert_tiles(ctypes.byref(cfg), ctypes.byref(tiles))
+    if rc != EP_OK:
+        raise EpError(rc, "ep_query_expert_tiles")
+    return tiles
 
 
 def _expert_sizes(cfg: EpExpertConfig) -> tuple:

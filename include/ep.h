@@ -441,6 +441,15 @@ typedef struct ep_expert_sizes {
 
 int ep_query_expert_sizes(const ep_expert_config_t *cfg, ep_expert_sizes_t *sizes);
 
+/* Rows of the tiles that the products of a configuration are computed in (32,
+ * 64, 128 or 256; 0 without rows, and for the gradients of fp8): which of the
+ * kernels a profile or a test of that configuration shows. */
+typedef struct ep_expert_tiles {
+    int32_t forward, d_x, d_w;
+} ep_expert_tiles_t;
+
+int ep_query_expert_tiles(const ep_expert_config_t *cfg, ep_expert_tiles_t *tiles);
+
 /* For each expert e and each of its rows r in [expert_base[e],
  * expert_base[e+1]):  pre[r] = x[r] W_e^T + bias[e],
  * out[r] = act(pre[r]) + residual[r].

@@ -611,3 +611,63 @@ def test_table_that_decreases_stays_inside():
     ep.ep_expert_mm_backward(cfg, base, None, w, d_out, ep.alloc_expert_backward(cfg), d_bias=db)
     torch.cuda.synchronize()
     assert (db[0] == 1).all() and (db[1:] == 0).all()
+
+
+# Sizes whose tiles (forward, d_x, d_w) those above leave out: ungated tiles of 256 x 256 with a tail of k, each
+# gradient in wide tiles beside the other in smaller ones, 128 x 128 tiles over more experts than lanes, and fp8 over
+# more steps than two of the scales' buffers hold.
+TILES = [([1500, 2500], 2440, 2056, "silu", (256, 256, 256)), ([2001, 0, 2000], 2432, 2056, "none", (256, 256, 128)),
+         ([800, 700], 2432, 2056, "relu", (64, 64, 256)),
+         ([k * 37 % 190 for k in range(70)], 1032, 520, "gelu", (128, 128, 128))]
+TILES_FP8 = [([1500, 2500], 2432, 2056, "none", 256), ([2001, 0, 2000], 2176, 1160, "swiglu", 256),
+             ([1500, 2500], 2304, 520, "swiglu", 128), ([800, 700], 2432, 2056, "silu", 64)]
+
+
+def test_tiles_of_the_large_tests():
+    """The sizes tested take the tiles they are there for."""
+    def tiles(counts, I, N, act, dtype="bf16"):
+        t = ep.ep_query_expert_tiles(ep.make_expert_config(len(counts), sum(counts) + 5, I, N, dtype, act))
+        return t.forward, t.d_x, t.d_w
+    assert [tiles(*t) for t in LARGE] == [(256, 256, 256), (128, 64, 128), (64, 128, 128)]
+    for t in TILES:
+        assert tiles(*t[:4]) == t[4]
+    for t in TILES_FP8:
+        assert tiles(*t[:4], dtype="fp8") == (t[4], 0, 0)
+    assert tiles([1, 0, 3, 2], 7168, 200, "swiglu", "fp8") == (32, 0, 0)
+    none = ep.ep_query_expert_tiles(ep.make_expert_config(4, 0, 64, 32))
+    assert (none.forward, none.d_x, none.d_w) == (0, 0, 0)
+    with pytest.raises(ep.EpError):
+        ep.ep_query_expert_tiles(ep.make_expert_config(4, 10, 64, 12))
+    cfg = ep.make_expert_config(4, 10, 64, 32)
+    assert ep._lib.ep_query_expert_tiles(ctypes.byref(cfg), None) == BAD
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,I,N,act,tiles", TILES)
+def test_large_in_the_other_tiles(counts, I, N, act, tiles):
+    test_large(counts, I, N, act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,I,N,act,tiles", TILES_FP8)
+def test_large_fp8_in_the_other_tiles(counts, I, N, act, tiles):
+    test_large_fp8(counts, I, N, act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("counts,I,N,act", [t[:4] for t in TILES] + LARGE[:1])
+def test_large_gradients_alone(counts, I, N, act):
+    """Either gradient of the rows or the weights without the other, bitwise as with it."""
+    print(f"[expert_mm_backward alone] {len(counts)} experts I={I} N={N} {act}", flush=True)
+    base, rows, x, w, g = make(counts, I, N, act, 23)
+    pre = torch.randn((rows, cols_of(N, act)), generator=g).bfloat16().cuda()
+    d = torch.randn((rows, N), generator=g).bfloat16().cuda()
+    x, w, bt = x.cuda(), w.cuda(), torch.tensor(base, dtype=torch.int32).cuda()
+    cfg = ep.make_expert_config(len(counts), rows, I, N, activation=act)
+    scratch = ep.alloc_expert_backward(cfg)
+    dx, dw = torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+    dx2, dw2 = torch.full_like(x, 7.0), torch.full_like(w, 7.0)
+    ep.ep_expert_mm_backward(cfg, bt, x, w, d, scratch, pre=pre, d_x=dx, d_w=dw)
+    ep.ep_expert_mm_backward(cfg, bt, None, w, d, scratch, pre=pre, d_x=dx2)
+    ep.ep_expert_mm_backward(cfg, bt, x, w, d, scratch, pre=pre, d_w=dw2)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
