@@ -671,3 +671,42 @@ def test_large_gradients_alone(counts, I, N, act):
     ep.ep_expert_mm_backward(cfg, bt, None, w, d, scratch, pre=pre, d_x=dx2)
     ep.ep_expert_mm_backward(cfg, bt, x, w, d, scratch, pre=pre, d_w=dw2)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("alignment", [1, 16])
+def test_fp8_rows_of_the_dispatch(alignment):
+    """fp8 tokens of two sources, dispatched, multiplied with the scales that the dispatch delivers, and combined."""
+    S, T, I, N, K, E, R = 2, 61, 384, 200, 3, 8, 4
+    g = torch.Generator().manual_seed(31)
+    x8 = torch.randn((S, T, I), generator=g).to(torch.float8_e4m3fn)
+    sf = torch.exp(torch.randn((S, T, I // 128), generator=g))
+    idx = torch.rand((S, T, E), generator=g).topk(K, 2).indices
+    idx[torch.rand((S, T, K), generator=g) < 0.1] = -1
+    weights = torch.rand((S, T, K), generator=g)
+    w8 = torch.randn((E, 2 * N, I), generator=g).to(torch.float8_e4m3fn)
+    ws = torch.exp(torch.randn((E, -(-2 * N // 128), I // 128), generator=g)) * I ** -0.5
+    cfg = ep.make_config(S, T, I, K, E, R, T, dtype="fp8", expand=True, alignment=alignment)
+    L, recv = ep.alloc_layout(cfg), ep.alloc_recv(cfg)
+    recv.recv_x.fill_(0x7f)  # NaN in every row that nothing writes
+    recv.recv_sf.fill_(float("nan"))
+    idx_d, weights_d = idx.cuda(), weights.cuda()
+    ep.ep_layout_dispatch(cfg, x8.cuda(), sf.cuda(), idx_d, weights_d, L, recv)
+    rows = recv.rows
+    out = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    kept = torch.full((rows, 2 * N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_mm(ep.make_expert_config(E, rows, I, N, dtype="fp8", activation="swiglu"), L.expert_base, recv.recv_x,
+                    w8.cuda(), out, x_sf=recv.recv_sf, w_sf=ws.cuda(), pre=kept)
+    tokens = torch.empty((S, T, N), dtype=torch.bfloat16, device="cuda")
+    ep.ep_combine(ep.make_config(S, T, N, K, E, R, T, expand=True, alignment=alignment), L, idx_d, weights_d, out, tokens)
+    torch.cuda.synchronize()
+    base, pos = L.expert_base.cpu().numpy(), L.expand_pos.cpu()
+    assert base[-1] % alignment == 0 and base[-1] <= rows
+    x64 = torch.zeros((rows, I), dtype=torch.float64)  # padding rows stay zero
+    for k in range(K):
+        there = idx[:, :, k] >= 0
+        x64[pos[:, :, k][there].long()] = (x8.double() * sf.double().repeat_interleave(128, 2))[there]
+    w64 = w8.double() * ws.double().repeat_interleave(128, 2).repeat_interleave(128, 1)[:, :2 * N]
+    check_forward(base, out, kept, *product64(base, x64, w64, None), I + 4, N, "swiglu", None)
+    y = torch.where((idx >= 0)[..., None], out.cpu().double()[pos.clamp(min=0).long()], 0.0) * weights.double()[..., None]
+    assert ((tokens.cpu().double() - y.sum(2)).abs() <= H * y.sum(2).abs() + (1 + H) * 2 * K * U * y.abs().sum(2)).all()

@@ -13,6 +13,8 @@ import os
 import pytest
 import torch
 
+import combine_ep_layout_07_amd.ep as ep
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 H = 2.0 ** -8
 
@@ -85,3 +87,77 @@ def test_layer_learns():
         layer.step(0.05)
         losses.append(err.square().sum(1).mean().item())
     assert losses[-1] < 0.98 * losses[0] and all(b < a * 1.01 for a, b in zip(losses, losses[1:]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("alignment", [1, 16])
+def test_layer_of_several_sources(alignment):
+    """Sources with padded tokens, sigmoid scores with a selection bias, biases in both products, and padding rows: the
+    calls of the layer, forward and backward, against autograd in 64 bits (tolerances as above)."""
+    S, T, hidden, inner, E, K, R, scale = 3, 50, 256, 136, 12, 3, 4, 1.5
+    print(f"[moe sources] S={S} T={T} alignment={alignment}", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+    x, d_out = rand(S, T, hidden).bfloat16(), rand(S, T, hidden).bfloat16()
+    up, down = (rand(E, 2 * inner, hidden) * hidden ** -0.5).bfloat16(), (rand(E, hidden, inner) * inner ** -0.5).bfloat16()
+    up_bias, down_bias, choice_bias = rand(E, 2 * inner) * 0.3, rand(E, hidden) * 0.3, rand(E) * 0.1
+    logits, d_balance = rand(S, T, E), torch.rand(S, generator=g, device="cuda") * T
+    mask = (torch.rand((S, T), generator=g, device="cuda") < 0.8).to(torch.uint8)
+
+    rc = ep.make_route_config(S, T, E, K, scoring="sigmoid", scale=scale)
+    cfg = ep.make_config(S, T, hidden, K, E, R, T, expand=True, alignment=alignment)
+    route, L, recv = ep.alloc_route(rc, balance=True), ep.alloc_layout(cfg), ep.alloc_recv(cfg)
+    recv.recv_x.fill_(0xff)  # NaN in every row that nothing writes
+    n = recv.rows
+    up_cfg = ep.make_expert_config(E, n, hidden, inner, activation="swiglu")
+    down_cfg = ep.make_expert_config(E, n, inner, hidden)
+
+    def nans(*shape):
+        return torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    pre, mid, y, out = nans(n, 2 * inner), nans(n, inner), nans(n, hidden), nans(S, T, hidden)
+    d_y, d_mid, d_rows, d_x = nans(n, hidden), nans(n, inner), nans(n, hidden), nans(S, T, hidden)
+    g_up, g_down, g_up_bias, g_down_bias = (torch.empty_like(t) for t in (up, down, up_bias, down_bias))
+    d_weights, d_logits = torch.empty((S, T, K), device="cuda"), torch.empty_like(logits)
+    rows = recv.recv_x.view(torch.bfloat16)
+    ep.ep_route(rc, logits, route, bias=choice_bias, token_mask=mask)
+    idx, base = route.topk_idx, L.expert_base
+    ep.ep_layout_dispatch(cfg, x, None, idx, route.topk_weights, L, recv)
+    ep.ep_expert_mm(up_cfg, base, rows, up, mid, bias=up_bias, pre=pre)
+    ep.ep_expert_mm(down_cfg, base, mid, down, y, bias=down_bias)
+    ep.ep_combine(cfg, L, idx, route.topk_weights, y, out)
+    ep.ep_combine_backward(cfg, L, idx, route.topk_weights, y, d_out, d_y, d_weights)
+    ep.ep_expert_mm_backward(down_cfg, base, mid, down, d_y, ep.alloc_expert_backward(down_cfg), d_x=d_mid, d_w=g_down,
+                             d_bias=g_down_bias)
+    ep.ep_expert_mm_backward(up_cfg, base, rows, up, d_mid, ep.alloc_expert_backward(up_cfg), pre=pre, d_x=d_rows, d_w=g_up,
+                             d_bias=g_up_bias)
+    ep.ep_combine(cfg, L, idx, torch.ones_like(route.topk_weights), d_rows, d_x)
+    ep.ep_route_backward(rc, logits, route, d_weights, d_balance, d_logits, token_mask=mask)
+    torch.cuda.synchronize()
+
+    leaves = [t.cpu().double().requires_grad_(True) for t in (x, logits, up, down, up_bias, down_bias)]
+    x64, l64, up64, down64, ub64, db64 = leaves
+    idx, keep = idx.cpu(), mask.cpu().double()
+    key = torch.where(keep[..., None] > 0, torch.sigmoid(l64.detach()) + choice_bias.cpu().double(), -1e9)
+    want = key.topk(K, 2).indices
+    assert torch.equal(idx.sort(2).values, torch.where(keep[..., None] > 0, want, -1).sort(2).values)
+    s = torch.sigmoid(l64) * keep[..., None]
+    sk = s.gather(2, idx.clamp(min=0))
+    weights = scale * sk / (sk.sum(2, keepdim=True) + 1e-20)
+    o = torch.zeros_like(x64)
+    for e in range(E):
+        a, t, k = torch.nonzero(idx == e, as_tuple=True)
+        p = x64[a, t] @ up64[e].t() + ub64[e]
+        r = (torch.nn.functional.silu(p[:, :inner]) * p[:, inner:]) @ down64[e].t() + db64[e]
+        o = o.index_put((a, t), weights[a, t, k][:, None] * r, accumulate=True)
+    v = keep.sum(1)
+    f = torch.stack([torch.bincount(idx[a][idx[a] >= 0], minlength=E) for a in range(S)]).double() * E / (K * v[:, None])
+    loss = (f * (s / (s.sum(2, keepdim=True) + 1e-20)).sum(1) / v[:, None]).sum(1)
+    ((o * d_out.cpu().double()).sum() + (loss * d_balance.cpu().double()).sum()).backward()
+    gx, gl, gu, gd, gub, gdb = (t.grad for t in leaves)
+    assert off(out, o.detach()) <= 6 * H
+    assert ((route.balance_loss.cpu().double() - loss.detach()).abs() <= 1e-5 * loss.detach()).all()
+    for got, w64 in ((d_x, gx), (g_up, gu), (g_down, gd), (g_up_bias, gub), (g_down_bias, gdb)):
+        assert off(got, w64) <= 12 * H
+    assert off(d_logits, gl) <= 0.25
