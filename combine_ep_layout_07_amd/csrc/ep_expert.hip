@@ -728,8 +728,11 @@ __global__ void __launch_bounds__(512, 2) k_expert_wide_back(ExpertArgs a, int c
     else wide_tile<kDw, false, 10>(a, block - dx, cols, smem, nullptr, nullptr);
 }
 
-// Gradient of the pre-activation, bf16, and the columns' sums of its unrounded
-// values for d_bias.  A workgroup takes 512 columns of one tile of kActRows
+// Gradient of the pre-activation and the columns' sums of its unrounded values
+// for d_bias.  It is stored as bf16, which the matrix unit takes: the error of d_x
+// and d_w against 64 bits is 0.0023 of their norm with an activation and 0.0017,
+// the results' own rounding, without; a second product with the remainder would
+// double their time.  A workgroup takes 512 columns of one tile of kActRows
 // rows of an expert (so that one expert with most of the rows is no slower),
 // each wave a quarter of the rows, four in flight; the waves' sums are added in
 // order, and a second launch adds the tiles' in order.
